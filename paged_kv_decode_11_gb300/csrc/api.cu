@@ -16,6 +16,7 @@
 #include "launch.h"
 #include "launch_prefill.h"
 #include "launch_cache.h"
+#include "host.h"
 #include "plan.h"
 #include "ptx.cuh"
 
@@ -38,6 +39,8 @@ bool current_device(int* dev) {
   if (cudaGetDevice(dev) != cudaSuccess) return false;
   return *dev >= 0 && *dev < kMaxDevices;
 }
+
+}  // namespace
 
 unsigned int* err_word() {
   int dev;
@@ -63,7 +66,7 @@ int sm_count() {
   return g_sms[dev];
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_encode == nullptr) {
     void* fn = nullptr;
@@ -77,9 +80,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return g_encode;
 }
 
-// Tensor map {D, 16, num_blocks * Hkv} over a cache [num_blocks, Hkv, 16, D]:
-// one box is 16 page rows by min(row bytes, 128) bytes, swizzled so that
-// the fragment loads of the kernels are bank-conflict free.
 // log2 of a block size the kernels take (1, 2, 4, ..., 64), or -1.
 int block_log2(int block_size) {
   for (int k = 0; k <= 6; ++k)
@@ -101,6 +101,8 @@ bool page_rows_fit(int num_blocks, int Hkv, int block_size, int max_blocks_per_s
 
 // A cache as the tensor maps see it: {D, 16 rows, num_blocks * Hkv * pages
 // per block} (innermost first); page row z = (block * Hkv + head) * ppb + sub.
+// One box is 16 page rows by min(row bytes, 128) bytes, swizzled so that the
+// fragment loads of the kernels are bank-conflict free.
 bool make_kv_tmap(CUtensorMap* m, const void* base, pkv_dtype dt, int D, int Hkv,
                   int num_blocks, int ppb_shift) {
   auto fn = encode_fn();
@@ -147,8 +149,6 @@ bool valid_dtypes(pkv_dtype q, pkv_dtype kv) {
   if (q != PKV_F16 && q != PKV_BF16) return false;
   return kv == q || kv == PKV_FP8_E4M3;
 }
-
-}  // namespace
 
 // One thread waits on an mbarrier with no arrivals, through the same bounded
 // wait the kernels use; when it gives up it records a timeout and returns.
