@@ -91,7 +91,13 @@ typedef enum {
   PKV_ERR_DEVICE_CHECK = 5   /* a device-side check failed (see below) */
 } pkv_status;
 
-typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype;
+typedef enum {
+  PKV_F16 = 0,
+  PKV_BF16 = 1,
+  PKV_FP8_E4M3 = 2,
+  PKV_FP8_E4M3_BLOCK = 3     /* E4M3 codes, one E8M0 scale per (block, KV head);
+                                rope_append_block_scaled and the _ext calls only */
+} pkv_dtype;
 
 /* Bits of the device error word. */
 #define PKV_DEVERR_BLOCK_ID   0x1u  /* block table entry outside [0, num_blocks) */
@@ -381,6 +387,121 @@ pkv_status rope_reshape_and_cache(void* query, const void* key, const void* valu
                                   int head_dim, int block_size, int num_blocks,
                                   const float* k_scales, const float* v_scales,
                                   void* stream);
+
+/*
+ * rope_append_block_scaled — appends new tokens to a paged cache that is held
+ * in E4M3 with one power-of-two scale per block of tokens and KV head
+ * (PKV_FP8_E4M3_BLOCK), the rotary embedding of their queries and keys applied
+ * on the way.
+ *   k_cache, v_cache: E4M3 codes [num_blocks, Hkv, BS, D]; k_scales, v_scales:
+ *           uint8 [num_blocks, Hkv], E8M0: a code stands for
+ *           code * 2^(scale - 127) (255 is NaN).
+ *   Sequence n appends rows cu_q_lens[n] .. cu_q_lens[n+1]-1 of key and value
+ *           ([total_q_tokens, Hkv, D] src_dtype): its L_n tokens at positions
+ *           P_n .. seq_lens[n]-1, P_n = seq_lens[n] - L_n (seq_lens includes
+ *           them); token at position j goes to block block_tables[n][j / BS],
+ *           offset j % BS. cu_q_lens does not decrease. L_n = 0 appends
+ *           nothing; rows outside every sequence are left alone.
+ *   The scale of a block and KV head, for K and for V:
+ *     need = the smallest e with amax <= 448 * 2^e, e >= -60, amax the largest
+ *            finite magnitude among the elements this call writes there;
+ *     a block whose offset 0 the call writes starts anew with scale need;
+ *     any other keeps its stored scale if that is at least need, and otherwise
+ *     takes need: then every slot of it that the call does not write is
+ *     re-encoded, code = E4M3(code * 2^(old - need)), exact unless the code
+ *     becomes subnormal.
+ *     The call's elements: code = E4M3(x * 2^-e), to nearest even, saturating
+ *     at +-448 (infinities saturate, NaN stays NaN; both leave amax alone).
+ *   cos_sin_cache: as in rope_reshape_and_cache, fp32 [max_position, rot_dim],
+ *           the row of a token being its position; or NULL for no rotation
+ *           (max_position, rot_dim, neox_style and the queries are then
+ *           ignored). Keys are rotated and rounded to src_dtype first.
+ *   query, query_out: [total_q_tokens, Hq, D] src_dtype, the rotated queries;
+ *           query_out may be query itself (in place), or both NULL.
+ *   A block that the call writes belongs to one sequence: copy a shared,
+ *   partly filled block before appending to it. (Two sequences that write one
+ *   block leave its contents undefined, nothing else.)
+ *   A sequence with L_n > seq_lens[n], a context past its row of block_tables
+ *   or rows outside the total_q_tokens sets PKV_DEVERR_QLEN, one with
+ *   seq_lens[n] > max_position sets PKV_DEVERR_POSITION, and is skipped whole
+ *   (its queries too); a block id outside [0, num_blocks) sets
+ *   PKV_DEVERR_BLOCK_ID and the tokens of that block are skipped.
+ *   D in {64, 128, 256}; BS 16, 32 or 64.
+ */
+pkv_status rope_append_block_scaled(const void* key, const void* value, pkv_dtype src_dtype,
+                                    void* k_cache, void* v_cache, uint8_t* k_scales,
+                                    uint8_t* v_scales, const int32_t* block_tables,
+                                    const int32_t* seq_lens, const int32_t* cu_q_lens,
+                                    int num_seqs, int total_q_tokens, void* query_out,
+                                    const void* query, const float* cos_sin_cache,
+                                    int max_position, int rot_dim, int neox_style,
+                                    int num_q_heads, int num_kv_heads, int head_dim,
+                                    int block_size, int max_blocks_per_seq, int num_blocks,
+                                    void* stream);
+
+/*
+ * paged_attn_decode_ext_workspace_size — bytes of workspace that
+ *   paged_attn_decode_ext needs (window as passed to it); 0 for invalid sizes.
+ *   The rules of paged_attn_decode_workspace_size apply.
+ */
+size_t paged_attn_decode_ext_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                            int head_dim, int max_seq_len, int window,
+                                            int partition_tokens);
+
+/*
+ * paged_attn_decode_ext — paged_attn_decode over a cache with block scales,
+ * or with modified scores, or both. For each sequence b, query head h (KV
+ * head g) and context position j:
+ *     x_j = scale * <q[b,h,:], K_j>
+ *     softcap > 0:   x_j = softcap * tanh(x_j / softcap)
+ *     alibi_slopes:  x_j = x_j - alibi_slopes[h] * (pos - j),  pos = seq_lens[b] - 1
+ *     window > 0:    only j with pos - j < window are seen
+ *     out = sum_j softmax(x)_j V_j,   lse = log sum_j exp(x_j)
+ *   kv_dtype PKV_FP8_E4M3_BLOCK: k_scales, v_scales are uint8
+ *   [num_blocks, Hkv] (see rope_append_block_scaled); PKV_FP8_E4M3: fp32 [Hkv];
+ *   otherwise ignored. softcap = 0, window = 0 and alibi_slopes = NULL (fp32
+ *   [Hq]) leave a step out. Blocks wholly outside a sequence's window are not
+ *   read, and their block table entries may hold anything.
+ *   scale is positive and finite, softcap finite. seq_lens[b] == 0 gives
+ *   out = 0, lse = -inf. BS 16, 32 or 64; everything else as
+ *   paged_attn_decode (workspace rules, partition_tokens, errors, programmatic
+ *   launch).
+ */
+pkv_status paged_attn_decode_ext(void* out, const void* q, pkv_dtype q_dtype,
+                                 const void* k_cache, const void* v_cache, pkv_dtype kv_dtype,
+                                 const int32_t* block_tables, const int32_t* seq_lens,
+                                 int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int block_size, int max_blocks_per_seq, int num_blocks,
+                                 int max_seq_len, float scale, const void* k_scales,
+                                 const void* v_scales, float softcap, int window,
+                                 const float* alibi_slopes, int partition_tokens,
+                                 float* out_lse, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * paged_attn_prefill_chunk_ext — paged_attn_prefill_chunk over a cache with
+ * block scales, or with modified scores, or both: the steps of
+ * paged_attn_decode_ext for every row of a chunk, with pos its position.
+ *   prefix_lens: optional int32 [num_seqs]: positions j < prefix_lens[n] are
+ *   seen by every row of sequence n, later ones included (a prefix that
+ *   attends both ways); values past seq_lens[n] mean the whole context, below
+ *   0 none. A row sees j < seq_lens[n] with j <= pos or j < prefix_lens[n],
+ *   and, with a window, pos - j < window; the distance of the bias is
+ *   |pos - j|. Blocks outside every row's window are not read.
+ *   A chunk with L_n > max_q_len sets PKV_DEVERR_QLEN and is skipped.
+ *   Everything else as paged_attn_prefill_chunk and paged_attn_decode_ext.
+ */
+pkv_status paged_attn_prefill_chunk_ext(void* out, const void* q, pkv_dtype q_dtype,
+                                        const void* k_cache, const void* v_cache,
+                                        pkv_dtype kv_dtype, const int32_t* block_tables,
+                                        const int32_t* seq_lens, const int32_t* cu_q_lens,
+                                        int num_seqs, int total_q_tokens, int max_q_len,
+                                        int num_q_heads, int num_kv_heads, int head_dim,
+                                        int block_size, int max_blocks_per_seq, int num_blocks,
+                                        float scale, const void* k_scales, const void* v_scales,
+                                        float softcap, int window, const float* alibi_slopes,
+                                        const int32_t* prefix_lens, float* out_lse,
+                                        void* stream);
 
 /*
  * pkv_get_device_error — synchronises `stream`, then reads and clears the

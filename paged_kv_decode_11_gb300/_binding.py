@@ -16,7 +16,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpkv.so")
 
-PKV_F16, PKV_BF16, PKV_FP8_E4M3 = 0, 1, 2
+PKV_F16, PKV_BF16, PKV_FP8_E4M3, PKV_FP8_E4M3_BLOCK = 0, 1, 2, 3
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration",
           3: "workspace missing or too small", 4: "CUDA error", 5: "device-side check failed"}
 DEVERR_BITS = {0x1: "block id", 0x2: "slot", 0x4: "seq_len", 0x8: "timeout", 0x10: "chunk length or rows",
@@ -26,7 +26,9 @@ DEVERR_BITS = {0x1: "block id", 0x2: "slot", 0x4: "seq_len", 0x8: "timeout", 0x1
 EXPORTS = ("paged_attn_decode_workspace_size", "paged_attn_decode", "paged_attn_decode_step",
            "paged_attn_decode_noalloc", "paged_attn_decode_noalloc_reset",
            "paged_attn_prefill_chunk", "paged_attn_varlen", "reshape_and_cache",
-           "rope_reshape_and_cache", "pkv_get_device_error", "pkv_status_string",
+           "rope_reshape_and_cache", "rope_append_block_scaled",
+           "paged_attn_decode_ext_workspace_size", "paged_attn_decode_ext",
+           "paged_attn_prefill_chunk_ext", "pkv_get_device_error", "pkv_status_string",
            "pkv_selftest_bounded_wait")
 
 _lib = None
@@ -75,6 +77,17 @@ def load(path: str = LIB_PATH):
     L.rope_reshape_and_cache.restype = I
     L.rope_reshape_and_cache.argtypes = [P, P, P, I, P, P, I, P, P, P, I, I, I, I, I, I, I, I,
                                          I, P, P, P]
+    L.rope_append_block_scaled.restype = I
+    L.rope_append_block_scaled.argtypes = [P, P, I, P, P, P, P, P, P, P, I, I, P, P, P, I, I, I, I,
+                                           I, I, I, I, I, P]
+    L.paged_attn_decode_ext_workspace_size.restype = S
+    L.paged_attn_decode_ext_workspace_size.argtypes = [I, I, I, I, I, I, I]
+    L.paged_attn_decode_ext.restype = I
+    L.paged_attn_decode_ext.argtypes = [P, P, I, P, P, I, P, P, I, I, I, I, I, I, I, I, F, P, P, F,
+                                        I, P, I, P, P, S, P]
+    L.paged_attn_prefill_chunk_ext.restype = I
+    L.paged_attn_prefill_chunk_ext.argtypes = [P, P, I, P, P, I, P, P, P, I, I, I, I, I, I, I, I, I,
+                                               F, P, P, F, I, P, P, P, P]
     L.pkv_get_device_error.restype = I
     L.pkv_get_device_error.argtypes = [P, ctypes.POINTER(ctypes.c_uint)]
     L.pkv_status_string.restype = ctypes.c_char_p
@@ -312,6 +325,189 @@ def rope_reshape_and_cache(query: torch.Tensor, key: torch.Tensor, value: torch.
         cos_sin_cache.shape[0], rot, int(bool(neox_style)), T, Hq, hkv, D, bs, nb,
         _dev_ptr(k_scales, "k_scales"), _dev_ptr(v_scales, "v_scales"), _stream(stream))
     _check("rope_reshape_and_cache", st)
+
+
+def _is_block_scale(t: Optional[torch.Tensor]) -> bool:
+    return t is not None and t.dtype in (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _expect(name: str, t: Optional[torch.Tensor], shape, dtypes, device) -> None:
+    """Raises ValueError unless t (None passes) has the shape, one of the dtypes and the device."""
+    if t is None:
+        return
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}")
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_E8M0 = (torch.uint8, torch.float8_e8m0fnu)
+_I32, _F32 = (torch.int32,), (torch.float32,)
+
+
+def _current_device(q: torch.Tensor, name: str) -> torch.device:
+    """The device a call runs on, the current one, which has to hold its tensors."""
+    if not q.is_cuda or q.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {q.device}, not on the current CUDA device")
+    return q.device
+
+
+def _attn_ext_tensors(out, q, k_cache, v_cache, block_tables, seq_lens, k_scales, v_scales,
+                      alibi_slopes, out_lse):
+    """Shape, dtype and device checks of the _ext attentions; returns the KV dtype code."""
+    dev = _current_device(q, "q")
+    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2 or seq_lens.dim() != 1:
+        raise ValueError("q is [rows, Hq, D], the caches [blocks, Hkv, BS, D], block_tables "
+                         "[sequences, blocks], seq_lens [sequences]")
+    rows, hq, d = q.shape
+    nb, hkv, bs, _ = k_cache.shape
+    n = seq_lens.shape[0]
+    block = _is_block_scale(k_scales)
+    if block and dtype_code(k_cache) != PKV_FP8_E4M3:
+        raise ValueError("block scales go with an E4M3 cache")
+    _expect("out", out, q.shape, (q.dtype,), dev)
+    _expect("k_cache", k_cache, (nb, hkv, bs, d), (k_cache.dtype,), dev)
+    _expect("v_cache", v_cache, k_cache.shape, (k_cache.dtype,), dev)
+    _expect("block_tables", block_tables, (n, block_tables.shape[1]), _I32, dev)
+    _expect("seq_lens", seq_lens, (n,), _I32, dev)
+    if dtype_code(k_cache) == PKV_FP8_E4M3:
+        shape, kinds = ((nb, hkv), _E8M0) if block else ((hkv,), _F32)
+        _expect("k_scales", k_scales, shape, kinds, dev)
+        _expect("v_scales", v_scales, shape, kinds, dev)
+    _expect("alibi_slopes", alibi_slopes, (hq,), _F32, dev)
+    _expect("out_lse", out_lse, (rows, hq), _F32, dev)
+    return PKV_FP8_E4M3_BLOCK if block else dtype_code(k_cache)
+
+
+def rope_append_block_scaled(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
+                             v_cache: torch.Tensor, k_scales: torch.Tensor,
+                             v_scales: torch.Tensor, block_tables: torch.Tensor,
+                             seq_lens: torch.Tensor, cu_q_lens: torch.Tensor,
+                             query: Optional[torch.Tensor] = None,
+                             query_out: Optional[torch.Tensor] = None,
+                             cos_sin_cache: Optional[torch.Tensor] = None,
+                             neox_style: bool = True, stream=None) -> None:
+    """Append key/value [T, Hkv, D] of sequences delimited by cu_q_lens [n + 1] to the E4M3
+    caches [num_blocks, Hkv, BS, D] with one E8M0 scale per block and KV head (k_scales,
+    v_scales: uint8 or float8_e8m0fnu [num_blocks, Hkv]). With cos_sin_cache fp32
+    [max_position, rot_dim] the keys are rotated on the way, and query [T, Hq, D] into
+    query_out (in place without one)."""
+    dev = _current_device(key, "key")
+    if key.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2 or seq_lens.dim() != 1:
+        raise ValueError("key is [rows, Hkv, D], the caches [blocks, Hkv, BS, D], block_tables "
+                         "[sequences, blocks], seq_lens [sequences]")
+    T, hkv, D = key.shape
+    nb, _, bs, _ = k_cache.shape
+    n = seq_lens.shape[0]
+    _expect("value", value, key.shape, (key.dtype,), dev)
+    _expect("k_cache", k_cache, (nb, hkv, bs, D), _CODES, dev)
+    _expect("v_cache", v_cache, k_cache.shape, _CODES, dev)
+    _expect("k_scales", k_scales, (nb, hkv), _E8M0, dev)
+    _expect("v_scales", v_scales, (nb, hkv), _E8M0, dev)
+    _expect("block_tables", block_tables, (n, block_tables.shape[1]), _I32, dev)
+    _expect("seq_lens", seq_lens, (n,), _I32, dev)
+    _expect("cu_q_lens", cu_q_lens, (n + 1,), _I32, dev)
+    hq, max_pos, rot = 1, 0, 0
+    if query is not None and cos_sin_cache is None:
+        raise ValueError("query needs cos_sin_cache")
+    if cos_sin_cache is not None:
+        if cos_sin_cache.dim() != 2:
+            raise ValueError("cos_sin_cache is [max_position, rot_dim]")
+        max_pos, rot = cos_sin_cache.shape
+        _expect("cos_sin_cache", cos_sin_cache, cos_sin_cache.shape, _F32, dev)
+    if query is not None:
+        if query.dim() != 3:
+            raise ValueError("query is [rows, Hq, D]")
+        hq = query.shape[1]
+        query_out = query if query_out is None else query_out
+        _expect("query", query, (T, hq, D), (key.dtype,), dev)
+        _expect("query_out", query_out, query.shape, (key.dtype,), dev)
+    elif query_out is not None:
+        raise ValueError("query_out needs query")
+    st = load().rope_append_block_scaled(
+        _dev_ptr(key, "key"), _dev_ptr(value, "value"), dtype_code(key),
+        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(k_scales, "k_scales"),
+        _dev_ptr(v_scales, "v_scales"), _dev_ptr(block_tables, "block_tables"),
+        _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(cu_q_lens, "cu_q_lens"), n, T,
+        _dev_ptr(query_out, "query_out"), _dev_ptr(query, "query"),
+        _dev_ptr(cos_sin_cache, "cos_sin_cache"), max_pos, rot, int(bool(neox_style)), hq, hkv, D,
+        bs, block_tables.shape[1], nb, _stream(stream))
+    _check("rope_append_block_scaled", st)
+
+
+def paged_attn_decode_ext_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                         head_dim: int, max_seq_len: int, window: int = 0,
+                                         partition_tokens: int = 0) -> int:
+    return int(load().paged_attn_decode_ext_workspace_size(
+        num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, window, partition_tokens))
+
+
+def paged_attn_decode_ext(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                          v_cache: torch.Tensor, block_tables: torch.Tensor,
+                          seq_lens: torch.Tensor, scale: float, max_seq_len: int,
+                          k_scales: Optional[torch.Tensor] = None,
+                          v_scales: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                          window: int = 0, alibi_slopes: Optional[torch.Tensor] = None,
+                          partition_tokens: int = 0, out_lse: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out[B, Hq, D] <- decode attention of q[B, Hq, D], the scores capped (softcap), biased by
+    distance (alibi_slopes fp32 [Hq]) or limited to the last `window` keys; k_scales/v_scales
+    uint8 or float8_e8m0fnu [num_blocks, Hkv] (block scales) or fp32 [Hkv] with an E4M3 cache.
+    Workspace rule as paged_attn_decode (paged_attn_decode_ext_workspace_size bytes)."""
+    kv = _attn_ext_tensors(out, q, k_cache, v_cache, block_tables, seq_lens, k_scales, v_scales,
+                           alibi_slopes, out_lse)
+    B, Hq, D = q.shape
+    nb, hkv, bs, _ = k_cache.shape
+    if seq_lens.shape[0] != B:
+        raise ValueError(f"q has {B} rows, seq_lens {seq_lens.shape[0]}")
+    if workspace is None:
+        ws = paged_attn_decode_ext_workspace_size(B, Hq, hkv, D, max_seq_len, window,
+                                                  partition_tokens)
+        workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=q.device)
+    elif workspace.device != q.device:
+        raise ValueError(f"workspace is on {workspace.device}, the call runs on {q.device}")
+    st = load().paged_attn_decode_ext(
+        _dev_ptr(out, "out"), _dev_ptr(q, "q"), dtype_code(q), _dev_ptr(k_cache, "k_cache"),
+        _dev_ptr(v_cache, "v_cache"), kv, _dev_ptr(block_tables, "block_tables"),
+        _dev_ptr(seq_lens, "seq_lens"), B, Hq, hkv, D, bs, block_tables.shape[1], nb,
+        int(max_seq_len), float(scale), _dev_ptr(k_scales, "k_scales"),
+        _dev_ptr(v_scales, "v_scales"), float(softcap), int(window),
+        _dev_ptr(alibi_slopes, "alibi_slopes"), int(partition_tokens),
+        _dev_ptr(out_lse, "out_lse"), _dev_ptr(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("paged_attn_decode_ext", st)
+
+
+def paged_attn_prefill_chunk_ext(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                                 v_cache: torch.Tensor, block_tables: torch.Tensor,
+                                 seq_lens: torch.Tensor, cu_q_lens: torch.Tensor, scale: float,
+                                 max_q_len: int, k_scales: Optional[torch.Tensor] = None,
+                                 v_scales: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                                 window: int = 0, alibi_slopes: Optional[torch.Tensor] = None,
+                                 prefix_lens: Optional[torch.Tensor] = None,
+                                 out_lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out[T, Hq, D] <- chunked-prefill attention of q[T, Hq, D] with the options of
+    paged_attn_decode_ext, and prefix_lens int32 [n]: positions below it are seen by every row
+    of their sequence."""
+    kv = _attn_ext_tensors(out, q, k_cache, v_cache, block_tables, seq_lens, k_scales, v_scales,
+                           alibi_slopes, out_lse)
+    T, Hq, D = q.shape
+    nb, hkv, bs, _ = k_cache.shape
+    n = seq_lens.shape[0]
+    _expect("cu_q_lens", cu_q_lens, (n + 1,), _I32, q.device)
+    _expect("prefix_lens", prefix_lens, (n,), _I32, q.device)
+    st = load().paged_attn_prefill_chunk_ext(
+        _dev_ptr(out, "out"), _dev_ptr(q, "q"), dtype_code(q), _dev_ptr(k_cache, "k_cache"),
+        _dev_ptr(v_cache, "v_cache"), kv, _dev_ptr(block_tables, "block_tables"),
+        _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(cu_q_lens, "cu_q_lens"), n, T, int(max_q_len), Hq,
+        hkv, D, bs, block_tables.shape[1], nb, float(scale), _dev_ptr(k_scales, "k_scales"),
+        _dev_ptr(v_scales, "v_scales"), float(softcap), int(window),
+        _dev_ptr(alibi_slopes, "alibi_slopes"), _dev_ptr(prefix_lens, "prefix_lens"),
+        _dev_ptr(out_lse, "out_lse"), _stream(stream))
+    _check("paged_attn_prefill_chunk_ext", st)
 
 
 def pkv_get_device_error(stream=None) -> int:
