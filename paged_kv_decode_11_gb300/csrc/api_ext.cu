@@ -175,9 +175,13 @@ pkv_status paged_attn_prefill_chunk_ext(void* out, const void* q, pkv_dtype q_dt
   const bool block_scaled = kv_dtype == PKV_FP8_E4M3_BLOCK;
   const pkv_dtype page_dtype = block_scaled ? PKV_FP8_E4M3 : kv_dtype;
   const int shift = page_shift(block_size);
-  CUtensorMap tmK, tmV;
+  CUtensorMap tmQ{}, tmK, tmV;
   if (!make_kv_tmap(&tmK, k_cache, page_dtype, head_dim, num_kv_heads, num_blocks, shift) ||
       !make_kv_tmap(&tmV, v_cache, page_dtype, head_dim, num_kv_heads, num_blocks, shift))
+    return PKV_ERR_CUDA;
+  const int G = num_q_heads / num_kv_heads;
+  if (page_dtype != PKV_FP8_E4M3 &&
+      !make_q_tmap(&tmQ, q, head_dim, num_q_heads, G, kPrefillTcRows / G, total_q_tokens))
     return PKV_ERR_CUDA;
   unsigned int* err = err_word();
   if (err == nullptr) return PKV_ERR_CUDA;
@@ -200,7 +204,7 @@ pkv_status paged_attn_prefill_chunk_ext(void* out, const void* q, pkv_dtype q_dt
   p.num_seqs = num_seqs;
   p.Hq = num_q_heads;
   p.Hkv = num_kv_heads;
-  p.G = num_q_heads / num_kv_heads;
+  p.G = G;
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   // no chunk is longer than the rows there are
@@ -213,7 +217,7 @@ pkv_status paged_attn_prefill_chunk_ext(void* out, const void* q, pkv_dtype q_dt
   ep.cap_log2 = softcap * kLog2eHost;
   ep.two_over_cap = softcap > 0.f ? 2.f / softcap : 0.f;
   ep.window = window;
-  return launch_prefill_ext(ep, head_dim, q_dtype, page_dtype, block_scaled, tmK, tmV,
+  return launch_prefill_ext(ep, head_dim, q_dtype, page_dtype, block_scaled, tmQ, tmK, tmV,
                             reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -1,6 +1,8 @@
 // prefill_ext.cu — chunked-prefill attention over E4M3 blocks with a scale per
 // block and KV head, and with modified scores (tanh cap, bias by distance,
-// window, prefix), with m16n8k16 products.
+// window, prefix): which kernel a call takes, and the one with m16n8k16
+// products, for E4M3 caches at head_dim 256 (whose query tile leaves the
+// tensor-core kernel's f16 rings no room, as in prefill.cu).
 //
 // Mathematics: decode_ext_kernel.cuh's for every row of a chunk; row i of a
 // chunk of L tokens on P cached ones stands at pos = P + i and sees the keys j
@@ -326,29 +328,23 @@ pkv_status launch_t(const PrefillExtParams& ep, const CUtensorMap& tmK, const CU
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-template <int D>
-pkv_status launch_d(const PrefillExtParams& p, pkv_dtype q_dtype, pkv_dtype kv_dtype, bool bsc,
-                    const CUtensorMap& tmK, const CUtensorMap& tmV, cudaStream_t stream) {
-  const bool qbf = q_dtype == PKV_BF16;
-  if (kv_dtype == PKV_FP8_E4M3) {
-    if (bsc)
-      return qbf ? launch_t<D, KV_E4M3, true, true>(p, tmK, tmV, stream)
-                 : launch_t<D, KV_E4M3, true, false>(p, tmK, tmV, stream);
-    return qbf ? launch_t<D, KV_E4M3, false, true>(p, tmK, tmV, stream)
-               : launch_t<D, KV_E4M3, false, false>(p, tmK, tmV, stream);
-  }
-  if (kv_dtype == PKV_BF16) return launch_t<D, KV_BF16, false, true>(p, tmK, tmV, stream);
-  return launch_t<D, KV_F16, false, false>(p, tmK, tmV, stream);
-}
-
 }  // namespace
 
 pkv_status launch_prefill_ext(const PrefillExtParams& p, int head_dim, pkv_dtype q_dtype,
-                              pkv_dtype kv_dtype, bool block_scaled, const CUtensorMap& tmK,
-                              const CUtensorMap& tmV, cudaStream_t stream) {
-  if (head_dim == 256) return launch_d<256>(p, q_dtype, kv_dtype, block_scaled, tmK, tmV, stream);
-  if (head_dim == 128) return launch_d<128>(p, q_dtype, kv_dtype, block_scaled, tmK, tmV, stream);
-  return launch_d<64>(p, q_dtype, kv_dtype, block_scaled, tmK, tmV, stream);
+                              pkv_dtype kv_dtype, bool block_scaled, const CUtensorMap& tmQ,
+                              const CUtensorMap& tmK, const CUtensorMap& tmV,
+                              cudaStream_t stream) {
+  if (prefill_tc_supported(head_dim, kv_dtype))
+    return block_scaled
+               ? launch_prefill_tc_block(p, head_dim, q_dtype, tmQ, tmK, tmV, stream)
+               : launch_prefill_tc_mod(p, head_dim, q_dtype, kv_dtype, tmQ, tmK, tmV, stream);
+  if (head_dim != 256 || kv_dtype != PKV_FP8_E4M3) return PKV_ERR_UNSUPPORTED;
+  const bool qbf = q_dtype == PKV_BF16;
+  if (block_scaled)
+    return qbf ? launch_t<256, KV_E4M3, true, true>(p, tmK, tmV, stream)
+               : launch_t<256, KV_E4M3, true, false>(p, tmK, tmV, stream);
+  return qbf ? launch_t<256, KV_E4M3, false, true>(p, tmK, tmV, stream)
+             : launch_t<256, KV_E4M3, false, false>(p, tmK, tmV, stream);
 }
 
 }  // namespace pkv
