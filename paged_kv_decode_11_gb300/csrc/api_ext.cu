@@ -277,7 +277,7 @@ pkv_status rope_append_block_scaled(const void* key, const void* value, pkv_dtyp
   p.rows = total_q_tokens;
   p.Hq = num_q_heads;
   p.Hkv = num_kv_heads;
-  p.D = head_dim;
+  p.d_log2 = head_dim == 64 ? 6 : head_dim == 128 ? 7 : 8;
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.bs_log2 = block_log2(block_size);

@@ -9,20 +9,32 @@
 //   exponent s if s >= e, else takes e and its other slots are re-encoded:
 //   code <- E4M3(code * 2^(s - e)). New codes are E4M3(x * 2^-e').
 //
+// Rotation: y1 = x1 c - x2 s, y2 = x2 c + x1 s, rounded once to the source type.
+// fp32 alone is not enough for that (its own rounding may move a sum across a
+// midpoint of the 16-bit type, about one element in 2^12 of f16), and doubles are
+// slow, so the sums are carried as unevaluated pairs: the products with their
+// errors (fma), their sum with its error (Knuth's two-sum), the parts added up.
+// The pair is then rounded to odd in fp32 - truncated, its last bit set if
+// anything was cut off - which leaves the second rounding, to 16 bits, the same as
+// one of the exact sum. y1 and y2 of a pair run through the packed two-float
+// instructions side by side.
+//
 // Work decomposition. Tokens of a sequence that fall into one block are
 // consecutive rows (a run of at most BS), so a run, not a token, is the unit:
 // its first row (the leader) starts a sequence's chunk or a block. A CTA takes
 // `window` consecutive rows and one KV head and does the runs whose leaders
-// lie among its rows; its first 64 threads do the keys, the other 64 the
-// values. A group goes over the run twice, 16 elements per thread and step: for
-// amax, then (the rows now in L1) to encode; the rotation is cheaper to repeat
-// than to keep. No two CTAs touch one block and head, so nothing is atomic and
-// the result does not depend on scheduling. The queries' CTAs follow in the same
-// grid, 16 elements a thread.
+// lie among its rows; its first 128 threads do the keys, the other 128 the
+// values. A group holds 4 x 16 elements of the run per thread in registers from
+// the maximum to the codes; of a longer run (64 tokens at head_dim 256) what
+// was not kept is loaded and rotated again. No two CTAs touch one block and
+// head, so nothing is atomic and the result does not depend on scheduling. The
+// queries follow in the same grid: a CTA takes a few rows, a thread keeps the
+// angles of its 16 dims and goes over the row's heads.
 //
 // Bound: bytes (16-bit rows in, 8-bit codes out, queries in and out) when the call is
 // long; for the tokens of a decode batch the chain of loads before the first
-// store (sequence, block id, scale, row) is what takes the time.
+// store (sequence, block id, scale) is what takes the time, so everything that
+// can be addressed without them is loaded first.
 #include "block_scale.cuh"
 #include "rope.cuh"
 #include "launch_ext.h"
@@ -30,8 +42,11 @@
 namespace pkv {
 namespace {
 
-constexpr int kGroup = 64;                 // threads on the keys, and on the values, of a run
-constexpr int kThreads = 2 * kGroup;
+// A CTA has GROUP threads on the keys of a run and GROUP on its values.
+constexpr int kShortGroup = 32, kLongGroup = 128;
+constexpr int kKeep = 4;                   // items (16 elements) a thread keeps of a run
+// Warps that share a row's query heads: four for few rows, one for many.
+constexpr int query_slices(int group) { return group == kLongGroup ? 1 : 4; }
 
 // The row's sequence n, its position and the rows of its chunk; n = -1 for rows
 // that no sequence owns or whose sequence is not valid (flagged elsewhere).
@@ -48,9 +63,12 @@ __device__ __forceinline__ bool seq_valid(const AppendBlockParams& p, int q0, in
 __device__ __forceinline__ RowPlace place_of(const AppendBlockParams& p, int row) {
   RowPlace r{-1, 0, 0, 0};
   // a decode batch has row n in sequence n: one round trip to see it
-  int n = row;
-  const bool guess = row < p.num_seqs;
-  int q0 = guess ? p.cu_q_lens[row] : -1, q1 = guess ? p.cu_q_lens[row + 1] : -1;
+  int n = row, q0 = -1, q1 = -1, ctx = 0;
+  if (row < p.num_seqs) {
+    q0 = p.cu_q_lens[row];
+    q1 = p.cu_q_lens[row + 1];
+    ctx = p.seq_lens[row];
+  }
   if (!(q0 <= row && row < q1)) {
     // the last n with cu_q_lens[n] <= row
     int lo = 0, hi = p.num_seqs + 1;       // cu[lo] <= row (if any), cu[hi] > row
@@ -64,8 +82,8 @@ __device__ __forceinline__ RowPlace place_of(const AppendBlockParams& p, int row
     q0 = p.cu_q_lens[n];
     q1 = p.cu_q_lens[n + 1];
     if (row < q0 || row >= q1) return r;
+    ctx = p.seq_lens[n];
   }
-  const int ctx = p.seq_lens[n];
   if (!seq_valid(p, q0, q1, ctx)) return r;
   r.n = n;
   r.q0 = q0;
@@ -116,26 +134,134 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float f) {
   return out;
 }
 
-// The 16 elements of item j of a head row, rotated where the row is a key or a
-// query and the item lies in the rotated part; o.a / o.b go to off_a / off_b.
-template <bool BF16, bool NEOX>
-__device__ __forceinline__ Pair8 take_item(const uint16_t* row, const float* cs, int rot, int j,
-                                           int& off_a, int& off_b) {
-  if (cs != nullptr && j < rot / 16) return rotate_item<BF16, NEOX>(row, cs, rot, j, off_a, off_b);
-  off_a = 16 * j;
-  off_b = 16 * j + 8;
-  return Pair8{*reinterpret_cast<const uint4*>(row + off_a),
-               *reinterpret_cast<const uint4*>(row + off_b)};
+// Two fp32 values in one register pair, for the packed instructions.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 sub2(f2 a, f2 b) {
+  f2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
+// r + rem (|rem| at most half a unit in r's last place) rounded to odd.
+__device__ __forceinline__ float round_odd(float r, float rem) {
+  const uint32_t b = __float_as_uint(r);
+  const bool cut = fabsf(rem) > 0.f;
+  const bool over = cut && (int32_t)(b ^ __float_as_uint(rem)) < 0;   // r lies past the sum
+  return __uint_as_float((b - (over ? 1u : 0u)) | (cut ? 1u : 0u));
+}
+
+// The angles of one item: 8 cosines and 8 sines.
+struct Angles {
+  float4 c[2], s[2];
+};
+
+__device__ __forceinline__ Angles load_angles(const float* cs, int half, int j) {
+  const float4* c = reinterpret_cast<const float4*>(cs + 8 * j);
+  const float4* s = reinterpret_cast<const float4*>(cs + half + 8 * j);
+  return Angles{{c[0], c[1]}, {s[0], s[1]}};
+}
+
+// (y1, y2) of each pair of an item, as described above.
 template <bool BF16, bool NEOX>
-__global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBlockParams p) {
+__device__ __forceinline__ Pair8 rotate_pairs(const Pair8& in, const Angles& an) {
+  float x1[8], x2[8];
+  item_pairs<BF16, NEOX>(in.a, in.b, x1, x2);
+  const float c[8] = {an.c[0].x, an.c[0].y, an.c[0].z, an.c[0].w,
+                      an.c[1].x, an.c[1].y, an.c[1].z, an.c[1].w};
+  const float s[8] = {an.s[0].x, an.s[0].y, an.s[0].z, an.s[0].w,
+                      an.s[1].x, an.s[1].y, an.s[1].z, an.s[1].w};
+  float y1[8], y2[8];
+  f2 finite = pack(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const f2 x = pack(x1[e], x2[e]), z = pack(x2[e], x1[e]);
+    const f2 cc = pack(c[e], c[e]), ss = pack(-s[e], s[e]);
+    // the rounded products by single multiplications: packed ones were merged into
+    // the additions below, whose error terms then belong to another sum
+    const float qa = __fmul_rn(x1[e], c[e]), qb = __fmul_rn(x2[e], c[e]);
+    const float pa = __fmul_rn(x2[e], -s[e]), pb = __fmul_rn(x1[e], s[e]);
+    const f2 nq = pack(-qa, -qb), p = pack(pa, pb), np = pack(-pa, -pb);
+    const f2 qe = fma2(x, cc, nq), pe = fma2(z, ss, np);             // what they leave
+    const f2 sum = sub2(p, nq);
+    const f2 bb = add2(sum, nq);
+    const f2 err = sub2(sub2(p, bb), add2(nq, sub2(sum, bb)));       // what the sum leaves
+    const f2 rest = add2(err, add2(qe, pe));
+    const f2 r = add2(sum, rest);
+    const f2 rem = sub2(rest, sub2(r, sum));
+    finite = fma2(r, pack(0.f, 0.f), finite);
+    const float2 rr = unpack(r), mm = unpack(rem);
+    y1[e] = round_odd(rr.x, mm.x);
+    y2[e] = round_odd(rr.y, mm.y);
+  }
+  const float2 f = unpack(finite);
+  if (!(f.x == 0.f && f.y == 0.f)) {
+    // an infinity or NaN among the inputs (the error terms are NaN then)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y1[e] = fmaf(x1[e], c[e], -(x2[e] * s[e]));
+      y2[e] = fmaf(x2[e], c[e], x1[e] * s[e]);
+    }
+  }
+  uint32_t w1[4], w2[4];                  // y of pairs 2 i and 2 i + 1
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (NEOX) {
+      w1[i] = pack2<BF16>(y1[2 * i], y1[2 * i + 1]);
+      w2[i] = pack2<BF16>(y2[2 * i], y2[2 * i + 1]);
+    } else {                              // pairs lie side by side: a holds 0..3, b 4..7
+      w1[i] = pack2<BF16>(y1[i], y2[i]);
+      w2[i] = pack2<BF16>(y1[4 + i], y2[4 + i]);
+    }
+  }
+  return Pair8{make_uint4(w1[0], w1[1], w1[2], w1[3]), make_uint4(w2[0], w2[1], w2[2], w2[3])};
+}
+
+// Where the two 8-element halves of item j of a head row lie: the partners of a
+// rotated item (rotate-half), or 16 consecutive elements.
+template <bool NEOX>
+__device__ __forceinline__ void item_offsets(int j, int rot, int& a, int& b) {
+  const bool halves = NEOX && j < rot / 16;
+  a = halves ? 8 * j : 16 * j;
+  b = halves ? 8 * j + rot / 2 : 16 * j + 8;
+}
+
+template <bool NEOX>
+__device__ __forceinline__ Pair8 load_item(const uint16_t* row, int j, int rot) {
+  int a, b;
+  item_offsets<NEOX>(j, rot, a, b);
+  return Pair8{*reinterpret_cast<const uint4*>(row + a), *reinterpret_cast<const uint4*>(row + b)};
+}
+
+template <bool BF16, bool NEOX, int GROUP>
+__global__ void __launch_bounds__(2 * GROUP, 512 / (2 * GROUP))
+    append_block_kernel(const __grid_constant__ AppendBlockParams p) {
+  constexpr int kGroup = GROUP, kThreads = 2 * GROUP, kSlices = query_slices(GROUP);
   // a decode launched behind this kernel may become resident now; it waits
   // for this grid to finish before it reads anything
   if (threadIdx.x == 0) griddep_launch_dependents();
-  __shared__ uint32_t s_max[4];
+  __shared__ uint32_t s_max[kThreads / 32];
   const int tid = threadIdx.x;
-  const int items = p.D / 16;               // of a head row
+  const int items_log2 = p.d_log2 - 4, items = 1 << items_log2;     // of a head row
 
   if (blockIdx.x < p.kv_ctas) {
     const int h = blockIdx.x % p.Hkv;
@@ -146,126 +272,201 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBloc
     uint8_t* cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache);
     uint8_t* scales = is_v ? p.v_scales : p.k_scales;
     const int bs = 1 << p.bs_log2;
-    for (int row = r0; row < min(p.rows, r0 + p.window); ++row) {
-      const RowPlace at = place_of(p, row);        // the same for every thread of the CTA
-      if (at.n < 0) continue;
-      const int off = at.pos & (bs - 1);
-      if (row != at.q0 && off != 0) continue;      // not the first row of a run
-      const int run = min(bs - off, at.ctx - at.pos);
-      const int id = p.block_tables[(int64_t)at.n * p.max_blocks + (at.pos >> p.bs_log2)];
-      if (id < 0 || id >= p.num_blocks) {
+    const int rot = is_v || p.cos_sin == nullptr ? 0 : p.rot;
+    const int64_t stride = (int64_t)p.Hkv << p.d_log2;
+    // a lane looks one row up; then the rows that lead a run are taken in turn
+    const int lane = tid & 31;
+    RowPlace mine{-1, 0, 0, 0};
+    if (lane < p.window && r0 + lane < p.rows) mine = place_of(p, r0 + lane);
+    uint32_t leaders = __ballot_sync(
+        0xffffffffu, mine.n >= 0 && (r0 + lane == mine.q0 || (mine.pos & (bs - 1)) == 0));
+    while (leaders != 0u) {                        // the same for every warp of the CTA
+      const int at = __ffs(leaders) - 1;
+      leaders &= leaders - 1u;
+      const int row = r0 + at;
+      const int n = __shfl_sync(0xffffffffu, mine.n, at);
+      const int pos = __shfl_sync(0xffffffffu, mine.pos, at);
+      const int ctx = __shfl_sync(0xffffffffu, mine.ctx, at);
+      const int off = pos & (bs - 1);
+      const int run = min(bs - off, ctx - pos);
+      const int count = run << items_log2;
+      const int id = p.block_tables[(int64_t)n * p.max_blocks + (pos >> p.bs_log2)];
+      const uint16_t* rows = src + ((int64_t)row * p.Hkv + h << p.d_log2);
+      // items t, t + 128, .. of chunk base .. base + 511 of the run, rotated
+      Pair8 x[kKeep];
+      auto take = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u) {
+          const int i = base + t + u * kGroup, k = i >> items_log2, j = i & (items - 1);
+          x[u] = i < count ? load_item<NEOX>(rows + k * stride, j, rot)
+                           : Pair8{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        }
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u) {
+          const int i = base + t + u * kGroup, k = i >> items_log2, j = i & (items - 1);
+          if (i < count && j < rot / 16)
+            x[u] = rotate_pairs<BF16, NEOX>(
+                x[u], load_angles(p.cos_sin + (int64_t)(pos + k) * p.rot, p.rot / 2, j));
+        }
+      };
+      uint32_t m = 0u;
+      int base = 0;
+      for (;; base += kKeep * kGroup) {
+        take(base);
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u)
+          m = finite_max<BF16>(finite_max<BF16>(m, x[u].a), x[u].b);
+        if (base + kKeep * kGroup >= count) break;
+      }
+      const bool known = id >= 0 && id < p.num_blocks;
+      const int64_t unit = known ? (int64_t)id * p.Hkv + h : 0;
+      const int stored =
+          off == 0 || !known ? -kE8M0Bias : min((int)scales[unit], 254) - kE8M0Bias;
+      m = __reduce_max_sync(0xffffffffu, m);
+      __syncthreads();                             // the run before has read s_max
+      if (lane == 0) s_max[tid >> 5] = m;
+      __syncthreads();
+      if (!known) {
         if (tid == 0 && h == 0) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
         continue;
       }
-      const int64_t unit = (int64_t)id * p.Hkv + h;
-      const int stored = off == 0 ? -kE8M0Bias : min((int)scales[unit], 254) - kE8M0Bias;
-      const uint16_t* rows = src + ((int64_t)row * p.Hkv + h) * p.D;
-      const int64_t stride = (int64_t)p.Hkv * p.D;
-      const float* cs = is_v || p.cos_sin == nullptr ? nullptr : p.cos_sin + (int64_t)at.pos * p.rot;
+#pragma unroll
+      for (int w = 0; w < kGroup / 32; ++w) m = max(m, s_max[(is_v ? kGroup / 32 : 0) + w]);
+      const int e = max(stored, block_exponent(widen16<BF16>(m)));
 
-      uint32_t m = 0u;
-      for (int i = t; i < run * items; i += kGroup) {
-        const int k = i / items, j = i - k * items;
-        int oa, ob;
-        const Pair8 x = take_item<BF16, NEOX>(rows + k * stride,
-                                              cs == nullptr ? nullptr : cs + (int64_t)k * p.rot,
-                                              p.rot, j, oa, ob);
-        m = finite_max<BF16>(finite_max<BF16>(m, x.a), x.b);
-      }
-      m = __reduce_max_sync(0xffffffffu, m);
-      if ((tid & 31) == 0) s_max[tid >> 5] = m;
-      __syncthreads();
-      m = max(s_max[is_v ? 2 : 0], s_max[is_v ? 3 : 1]);
-      __syncthreads();                             // the next run reuses s_max
-      const int need = block_exponent(widen16<BF16>(m));
-      const int e = max(stored, need);
-
-      uint8_t* block = cache + (unit << p.bs_log2) * p.D;
+      uint8_t* block = cache + (unit << (p.bs_log2 + p.d_log2));
       if (off != 0 && e > stored) {
         // the slots before and behind the run, to the new scale
         const float f = pow2_any(max(stored - e, -126));
-        const int cpr = p.D / 16;
-        for (int i = t; i < (bs - run) * cpr; i += kGroup) {
-          int k = i / cpr;
+        for (int i = t; i < (bs - run) << items_log2; i += kGroup) {
+          int k = i >> items_log2;
           if (k >= off) k += run;
-          uint4* c = reinterpret_cast<uint4*>(block + (int64_t)k * p.D + 16 * (i % cpr));
+          uint4* c = reinterpret_cast<uint4*>(block + (k << p.d_log2) + 16 * (i & (items - 1)));
           const uint4 w = *c;
           *c = make_uint4(rescale_e4m3x4(w.x, f), rescale_e4m3x4(w.y, f), rescale_e4m3x4(w.z, f),
                           rescale_e4m3x4(w.w, f));
         }
       }
       const float inv = pow2_any(-e);
-      for (int i = t; i < run * items; i += kGroup) {
-        const int k = i / items, j = i - k * items;
-        int oa, ob;
-        const Pair8 x = take_item<BF16, NEOX>(rows + k * stride,
-                                              cs == nullptr ? nullptr : cs + (int64_t)k * p.rot,
-                                              p.rot, j, oa, ob);
-        uint8_t* dst = block + (int64_t)(off + k) * p.D;
-        *reinterpret_cast<uint2*>(dst + oa) = encode_pow2_x8<BF16>(x.a, inv);
-        *reinterpret_cast<uint2*>(dst + ob) = encode_pow2_x8<BF16>(x.b, inv);
+      for (;;) {                                   // the last chunk is still there
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u) {
+          const int i = base + t + u * kGroup, k = i >> items_log2, j = i & (items - 1);
+          if (i >= count) continue;
+          int a, b;
+          item_offsets<NEOX>(j, rot, a, b);
+          uint8_t* dst = block + ((off + k) << p.d_log2);
+          const uint2 ca = encode_pow2_x8<BF16>(x[u].a, inv), cb = encode_pow2_x8<BF16>(x[u].b, inv);
+          *reinterpret_cast<uint2*>(dst + a) = ca;
+          *reinterpret_cast<uint2*>(dst + b) = cb;
+        }
+        if (base == 0) break;
+        base -= kKeep * kGroup;
+        take(base);
       }
       if (t == 0) scales[unit] = (uint8_t)(e + kE8M0Bias);
     }
     return;
   }
 
-  // ---- queries: one thread per 16 elements --------------------------------------------
-  const int64_t base = (int64_t)(blockIdx.x - p.kv_ctas) * kThreads;
-  if (base == 0) {
+  // ---- queries --------------------------------------------------------------------------
+  const unsigned int cta = blockIdx.x - p.kv_ctas;
+  if (cta == 0) {
     // one CTA looks every sequence over and says what is wrong with it
     for (int n = tid; n < p.num_seqs; n += kThreads) {
-      const int q0 = p.cu_q_lens[n], q1 = p.cu_q_lens[n + 1], ctx = p.seq_lens[n];
-      if (!seq_valid(p, q0, q1, ctx) && q0 != q1) {
+      const int c0 = p.cu_q_lens[n], c1 = p.cu_q_lens[n + 1], ctx = p.seq_lens[n];
+      if (!seq_valid(p, c0, c1, ctx) && c0 != c1) {
         const bool past = p.cos_sin != nullptr && ctx > p.max_position;
         atomicOr(p.err, past ? PKV_DEVERR_POSITION : PKV_DEVERR_QLEN);
       }
     }
   }
   if (p.query_out == nullptr) return;
-  const int64_t i = base + tid;
-  const int per_row = p.Hq * items;
-  const int64_t row = i / per_row;
+  const int lane = tid & 31;
+  const int64_t task = (int64_t)cta * (kThreads / 32) + (tid >> 5);
+  const int row = (int)(task / kSlices), slice = (int)(task % kSlices);
   if (row >= p.rows) return;
-  const RowPlace at = place_of(p, (int)row);
+  const int64_t o = (int64_t)row * p.Hq << p.d_log2;
+  const uint16_t* q = static_cast<const uint16_t*>(p.query) + o;
+  uint16_t* out = static_cast<uint16_t*>(p.query_out) + o;
+  // the rotated items: lane = (head, item j) with as many heads at a time as fit, j
+  // and its angles staying; the warp's heads advance by `step`
+  const int R = p.rot / 16, per = 32 / R, step = per * kSlices;
+  const int j = lane % R;
+  const int h_end = lane < per * R ? p.Hq : 0;
+  int h0 = slice * per + lane / R;
+  constexpr int U = 4;
+  Pair8 x[U];
+  auto load = [&]() {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h0 + u * step < h_end)
+        x[u] = load_item<NEOX>(q + ((h0 + u * step) << p.d_log2), j, p.rot);
+  };
+  load();
+  const RowPlace at = place_of(p, row);
   if (at.n < 0) return;
-  const int rest = (int)(i - row * per_row);
-  const int hq = rest / items, j = rest - hq * items;
-  const int64_t o = (row * p.Hq + hq) * p.D;
-  int oa, ob;
-  const Pair8 x = take_item<BF16, NEOX>(static_cast<const uint16_t*>(p.query) + o,
-                                        p.cos_sin + (int64_t)at.pos * p.rot, p.rot, j, oa, ob);
-  uint16_t* dst = static_cast<uint16_t*>(p.query_out) + o;
-  *reinterpret_cast<uint4*>(dst + oa) = x.a;
-  *reinterpret_cast<uint4*>(dst + ob) = x.b;
+  const Angles an = load_angles(p.cos_sin + (int64_t)at.pos * p.rot, p.rot / 2, j);
+  int a, b;
+  item_offsets<NEOX>(j, p.rot, a, b);
+  while (h0 < h_end) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * step;
+      if (h >= h_end) continue;
+      const Pair8 y = rotate_pairs<BF16, NEOX>(x[u], an);
+      *reinterpret_cast<uint4*>(out + (h << p.d_log2) + a) = y.a;
+      *reinterpret_cast<uint4*>(out + (h << p.d_log2) + b) = y.b;
+    }
+    h0 += U * step;
+    load();
+  }
+  // the dims behind the rotated ones, 8 at a time (in place they are there already)
+  const int chunks = (1 << (p.d_log2 - 3)) - 2 * R;
+  if (q == out || chunks == 0) return;
+  for (int i = slice * 32 + lane; i < p.Hq * chunks; i += 32 * kSlices) {
+    const int h = i / chunks, d = p.rot + 8 * (i - h * chunks);
+    *reinterpret_cast<uint4*>(out + (h << p.d_log2) + d) =
+        *reinterpret_cast<const uint4*>(q + (h << p.d_log2) + d);
+  }
 }
 
 }  // namespace
+
+template <int GROUP>
+static void launch_group(AppendBlockParams& p, pkv_dtype src_dtype, unsigned int grid,
+                         cudaStream_t stream) {
+  const bool neox = p.cos_sin == nullptr || p.neox != 0;
+  constexpr int T = 2 * GROUP;
+  if (src_dtype == PKV_BF16) {
+    if (neox) append_block_kernel<true, true, GROUP><<<grid, T, 0, stream>>>(p);
+    else append_block_kernel<true, false, GROUP><<<grid, T, 0, stream>>>(p);
+  } else {
+    if (neox) append_block_kernel<false, true, GROUP><<<grid, T, 0, stream>>>(p);
+    else append_block_kernel<false, false, GROUP><<<grid, T, 0, stream>>>(p);
+  }
+}
 
 pkv_status launch_append_block(const AppendBlockParams& params, pkv_dtype src_dtype,
                                cudaStream_t stream) {
   AppendBlockParams p = params;
   if (p.rows == 0) return PKV_OK;
-  // rows per cache-write CTA: one while that gives at most some thousand CTAs
-  // (most rows of a decode batch lead a run), up to 16 when rows are many (then
-  // most do not, and a CTA per row would be spent finding that out)
+  // rows per cache-write CTA: about as many as a run has on average (at most
+  // rows / BS + num_seqs rows lead one), so that a CTA meets one leader, not
+  // none (a CTA spent finding that out) and not several (done in turn)
+  const int64_t leaders = ((int64_t)p.rows >> p.bs_log2) + p.num_seqs;
   p.window = 1;
-  while (p.window < 16 && (int64_t)p.rows * p.Hkv > (int64_t)8192 * p.window) p.window *= 2;
+  while (p.window < 32 && 2 * p.window * leaders <= p.rows) p.window *= 2;
+  // a warp on the keys of a run while runs may be single tokens, four for chunks
+  const bool is_short = p.window == 1;
+  const int group = is_short ? kShortGroup : kLongGroup;
   const int64_t kv = (((int64_t)p.rows + p.window - 1) / p.window) * p.Hkv;
-  const int64_t q = p.query_out == nullptr
-                        ? 1
-                        : ((int64_t)p.rows * p.Hq * (p.D / 16) + kThreads - 1) / kThreads;
+  const int64_t warps = (int64_t)p.rows * query_slices(group), wpc = 2 * group / 32;
+  const int64_t q = p.query_out == nullptr ? 1 : (warps + wpc - 1) / wpc;
   if (kv + q > 0x7FFFFFFF) return PKV_ERR_INVALID_ARG;
   p.kv_ctas = (unsigned int)kv;
-  const unsigned int grid = (unsigned int)(kv + q);
-  const bool neox = p.cos_sin == nullptr || p.neox != 0;
-  if (src_dtype == PKV_BF16) {
-    if (neox) append_block_kernel<true, true><<<grid, kThreads, 0, stream>>>(p);
-    else append_block_kernel<true, false><<<grid, kThreads, 0, stream>>>(p);
-  } else {
-    if (neox) append_block_kernel<false, true><<<grid, kThreads, 0, stream>>>(p);
-    else append_block_kernel<false, false><<<grid, kThreads, 0, stream>>>(p);
-  }
+  if (is_short) launch_group<kShortGroup>(p, src_dtype, (unsigned int)(kv + q), stream);
+  else launch_group<kLongGroup>(p, src_dtype, (unsigned int)(kv + q), stream);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -22,9 +22,10 @@ struct AppendBlockParams {
   const float* cos_sin;         // null: no rotation
   unsigned int* err;
   int64_t max_position;         // longest context that the rotary table covers
-  int rot, neox, num_seqs, rows, Hq, Hkv, D, max_blocks, num_blocks;
+  int rot, neox, num_seqs, rows, Hq, Hkv, max_blocks, num_blocks;
+  int d_log2;                   // log2(head_dim)
   int bs_log2;                  // log2(block_size), 4 to 6
-  int window;                   // tokens per cache-write CTA
+  int window;                   // rows per cache-write CTA (at most 32)
   unsigned int kv_ctas;         // cache-write CTAs, the first of the grid
 };
 
