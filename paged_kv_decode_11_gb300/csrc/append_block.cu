@@ -253,7 +253,7 @@ __device__ __forceinline__ Pair8 load_item(const uint16_t* row, int j, int rot) 
 }
 
 template <bool BF16, bool NEOX, int GROUP>
-__global__ void __launch_bounds__(2 * GROUP, 512 / (2 * GROUP))
+__global__ void __launch_bounds__(2 * GROUP, GROUP == kLongGroup ? 3 : 8)
     append_block_kernel(const __grid_constant__ AppendBlockParams p) {
   constexpr int kGroup = GROUP, kThreads = 2 * GROUP, kSlices = query_slices(GROUP);
   // a decode launched behind this kernel may become resident now; it waits
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(2 * GROUP, 512 / (2 * GROUP))
   const int j = lane % R;
   const int h_end = lane < per * R ? p.Hq : 0;
   int h0 = slice * per + lane / R;
-  constexpr int U = 4;
+  constexpr int U = 2;
   Pair8 x[U];
   auto load = [&]() {
 #pragma unroll
