@@ -1,4 +1,6 @@
-"""Thin ctypes binding of libpkv (include/pkv.h), same names as the C ABI.
+"""Thin binding of libpkv (include/pkv.h), same names as the C ABI: ctypes, and
+for the block-scaled append and the _ext attentions the _native module
+(csrc/native.cpp), which reads the tensors in a fraction of the time.
 
 Only argument marshalling happens here: torch tensors become device pointers,
 shapes and dtype codes; every step of the computation runs in the library's
@@ -32,6 +34,7 @@ EXPORTS = ("paged_attn_decode_workspace_size", "paged_attn_decode", "paged_attn_
            "pkv_selftest_bounded_wait")
 
 _lib = None
+_native = None
 
 
 class PkvError(RuntimeError):
@@ -46,7 +49,7 @@ class PkvError(RuntimeError):
 
 def load(path: str = LIB_PATH):
     """Load libpkv.so and declare its signatures. Raises if it is absent."""
-    global _lib
+    global _lib, _native
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -94,6 +97,14 @@ def load(path: str = LIB_PATH):
     L.pkv_status_string.argtypes = [I]
     L.pkv_selftest_bounded_wait.restype = I
     L.pkv_selftest_bounded_wait.argtypes = [ctypes.c_uint, P]
+    try:
+        from . import _native as native
+    except ImportError as e:
+        raise RuntimeError("_native not built; run paged_kv_decode_11_gb300.build.build()") from e
+    native.bind(*[ctypes.cast(f, P).value for f in (L.paged_attn_decode_ext,
+                                                    L.paged_attn_prefill_chunk_ext,
+                                                    L.rope_append_block_scaled)])
+    _native = native
     _lib = L
     return L
 
@@ -327,59 +338,11 @@ def rope_reshape_and_cache(query: torch.Tensor, key: torch.Tensor, value: torch.
     _check("rope_reshape_and_cache", st)
 
 
-def _is_block_scale(t: Optional[torch.Tensor]) -> bool:
-    return t is not None and t.dtype in (torch.uint8, torch.float8_e8m0fnu)
-
-
-def _expect(name: str, t: Optional[torch.Tensor], shape, dtypes, device) -> None:
-    """Raises ValueError unless t (None passes) has the shape, one of the dtypes and the device."""
-    if t is None:
-        return
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} has dtype {t.dtype}")
-
-
-_CODES = (torch.uint8, torch.float8_e4m3fn)
-_E8M0 = (torch.uint8, torch.float8_e8m0fnu)
-_I32, _F32 = (torch.int32,), (torch.float32,)
-
-
-def _current_device(q: torch.Tensor, name: str) -> torch.device:
-    """The device a call runs on, the current one, which has to hold its tensors."""
-    if not q.is_cuda or q.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {q.device}, not on the current CUDA device")
-    return q.device
-
-
-def _attn_ext_tensors(out, q, k_cache, v_cache, block_tables, seq_lens, k_scales, v_scales,
-                      alibi_slopes, out_lse):
-    """Shape, dtype and device checks of the _ext attentions; returns the KV dtype code."""
-    dev = _current_device(q, "q")
-    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2 or seq_lens.dim() != 1:
-        raise ValueError("q is [rows, Hq, D], the caches [blocks, Hkv, BS, D], block_tables "
-                         "[sequences, blocks], seq_lens [sequences]")
-    rows, hq, d = q.shape
-    nb, hkv, bs, _ = k_cache.shape
-    n = seq_lens.shape[0]
-    block = _is_block_scale(k_scales)
-    if block and dtype_code(k_cache) != PKV_FP8_E4M3:
-        raise ValueError("block scales go with an E4M3 cache")
-    _expect("out", out, q.shape, (q.dtype,), dev)
-    _expect("k_cache", k_cache, (nb, hkv, bs, d), (k_cache.dtype,), dev)
-    _expect("v_cache", v_cache, k_cache.shape, (k_cache.dtype,), dev)
-    _expect("block_tables", block_tables, (n, block_tables.shape[1]), _I32, dev)
-    _expect("seq_lens", seq_lens, (n,), _I32, dev)
-    if dtype_code(k_cache) == PKV_FP8_E4M3:
-        shape, kinds = ((nb, hkv), _E8M0) if block else ((hkv,), _F32)
-        _expect("k_scales", k_scales, shape, kinds, dev)
-        _expect("v_scales", v_scales, shape, kinds, dev)
-    _expect("alibi_slopes", alibi_slopes, (hq,), _F32, dev)
-    _expect("out_lse", out_lse, (rows, hq), _F32, dev)
-    return PKV_FP8_E4M3_BLOCK if block else dtype_code(k_cache)
+def _handle(stream) -> Optional[int]:
+    """The stream argument as _native takes it: None is the current stream."""
+    if stream is None or type(stream) is int:
+        return stream
+    return _stream(stream)
 
 
 def rope_append_block_scaled(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
@@ -395,46 +358,10 @@ def rope_append_block_scaled(key: torch.Tensor, value: torch.Tensor, k_cache: to
     v_scales: uint8 or float8_e8m0fnu [num_blocks, Hkv]). With cos_sin_cache fp32
     [max_position, rot_dim] the keys are rotated on the way, and query [T, Hq, D] into
     query_out (in place without one)."""
-    dev = _current_device(key, "key")
-    if key.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2 or seq_lens.dim() != 1:
-        raise ValueError("key is [rows, Hkv, D], the caches [blocks, Hkv, BS, D], block_tables "
-                         "[sequences, blocks], seq_lens [sequences]")
-    T, hkv, D = key.shape
-    nb, _, bs, _ = k_cache.shape
-    n = seq_lens.shape[0]
-    _expect("value", value, key.shape, (key.dtype,), dev)
-    _expect("k_cache", k_cache, (nb, hkv, bs, D), _CODES, dev)
-    _expect("v_cache", v_cache, k_cache.shape, _CODES, dev)
-    _expect("k_scales", k_scales, (nb, hkv), _E8M0, dev)
-    _expect("v_scales", v_scales, (nb, hkv), _E8M0, dev)
-    _expect("block_tables", block_tables, (n, block_tables.shape[1]), _I32, dev)
-    _expect("seq_lens", seq_lens, (n,), _I32, dev)
-    _expect("cu_q_lens", cu_q_lens, (n + 1,), _I32, dev)
-    hq, max_pos, rot = 1, 0, 0
-    if query is not None and cos_sin_cache is None:
-        raise ValueError("query needs cos_sin_cache")
-    if cos_sin_cache is not None:
-        if cos_sin_cache.dim() != 2:
-            raise ValueError("cos_sin_cache is [max_position, rot_dim]")
-        max_pos, rot = cos_sin_cache.shape
-        _expect("cos_sin_cache", cos_sin_cache, cos_sin_cache.shape, _F32, dev)
-    if query is not None:
-        if query.dim() != 3:
-            raise ValueError("query is [rows, Hq, D]")
-        hq = query.shape[1]
-        query_out = query if query_out is None else query_out
-        _expect("query", query, (T, hq, D), (key.dtype,), dev)
-        _expect("query_out", query_out, query.shape, (key.dtype,), dev)
-    elif query_out is not None:
-        raise ValueError("query_out needs query")
-    st = load().rope_append_block_scaled(
-        _dev_ptr(key, "key"), _dev_ptr(value, "value"), dtype_code(key),
-        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(k_scales, "k_scales"),
-        _dev_ptr(v_scales, "v_scales"), _dev_ptr(block_tables, "block_tables"),
-        _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(cu_q_lens, "cu_q_lens"), n, T,
-        _dev_ptr(query_out, "query_out"), _dev_ptr(query, "query"),
-        _dev_ptr(cos_sin_cache, "cos_sin_cache"), max_pos, rot, int(bool(neox_style)), hq, hkv, D,
-        bs, block_tables.shape[1], nb, _stream(stream))
+    if _native is None:
+        load()
+    st = _native.append(key, value, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens,
+                        cu_q_lens, query, query_out, cos_sin_cache, neox_style, _handle(stream))
     _check("rope_append_block_scaled", st)
 
 
@@ -457,27 +384,16 @@ def paged_attn_decode_ext(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Ten
     distance (alibi_slopes fp32 [Hq]) or limited to the last `window` keys; k_scales/v_scales
     uint8 or float8_e8m0fnu [num_blocks, Hkv] (block scales) or fp32 [Hkv] with an E4M3 cache.
     Workspace rule as paged_attn_decode (paged_attn_decode_ext_workspace_size bytes)."""
-    kv = _attn_ext_tensors(out, q, k_cache, v_cache, block_tables, seq_lens, k_scales, v_scales,
-                           alibi_slopes, out_lse)
-    B, Hq, D = q.shape
-    nb, hkv, bs, _ = k_cache.shape
-    if seq_lens.shape[0] != B:
-        raise ValueError(f"q has {B} rows, seq_lens {seq_lens.shape[0]}")
+    if _native is None:
+        load()
     if workspace is None:
-        ws = paged_attn_decode_ext_workspace_size(B, Hq, hkv, D, max_seq_len, window,
+        B, Hq, D = q.shape
+        ws = paged_attn_decode_ext_workspace_size(B, Hq, k_cache.shape[1], D, max_seq_len, window,
                                                   partition_tokens)
         workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=q.device)
-    elif workspace.device != q.device:
-        raise ValueError(f"workspace is on {workspace.device}, the call runs on {q.device}")
-    st = load().paged_attn_decode_ext(
-        _dev_ptr(out, "out"), _dev_ptr(q, "q"), dtype_code(q), _dev_ptr(k_cache, "k_cache"),
-        _dev_ptr(v_cache, "v_cache"), kv, _dev_ptr(block_tables, "block_tables"),
-        _dev_ptr(seq_lens, "seq_lens"), B, Hq, hkv, D, bs, block_tables.shape[1], nb,
-        int(max_seq_len), float(scale), _dev_ptr(k_scales, "k_scales"),
-        _dev_ptr(v_scales, "v_scales"), float(softcap), int(window),
-        _dev_ptr(alibi_slopes, "alibi_slopes"), int(partition_tokens),
-        _dev_ptr(out_lse, "out_lse"), _dev_ptr(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+    st = _native.decode_ext(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len,
+                            k_scales, v_scales, softcap, window, alibi_slopes, partition_tokens,
+                            out_lse, workspace, _handle(stream))
     _check("paged_attn_decode_ext", st)
 
 
@@ -492,21 +408,11 @@ def paged_attn_prefill_chunk_ext(out: torch.Tensor, q: torch.Tensor, k_cache: to
     """out[T, Hq, D] <- chunked-prefill attention of q[T, Hq, D] with the options of
     paged_attn_decode_ext, and prefix_lens int32 [n]: positions below it are seen by every row
     of their sequence."""
-    kv = _attn_ext_tensors(out, q, k_cache, v_cache, block_tables, seq_lens, k_scales, v_scales,
-                           alibi_slopes, out_lse)
-    T, Hq, D = q.shape
-    nb, hkv, bs, _ = k_cache.shape
-    n = seq_lens.shape[0]
-    _expect("cu_q_lens", cu_q_lens, (n + 1,), _I32, q.device)
-    _expect("prefix_lens", prefix_lens, (n,), _I32, q.device)
-    st = load().paged_attn_prefill_chunk_ext(
-        _dev_ptr(out, "out"), _dev_ptr(q, "q"), dtype_code(q), _dev_ptr(k_cache, "k_cache"),
-        _dev_ptr(v_cache, "v_cache"), kv, _dev_ptr(block_tables, "block_tables"),
-        _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(cu_q_lens, "cu_q_lens"), n, T, int(max_q_len), Hq,
-        hkv, D, bs, block_tables.shape[1], nb, float(scale), _dev_ptr(k_scales, "k_scales"),
-        _dev_ptr(v_scales, "v_scales"), float(softcap), int(window),
-        _dev_ptr(alibi_slopes, "alibi_slopes"), _dev_ptr(prefix_lens, "prefix_lens"),
-        _dev_ptr(out_lse, "out_lse"), _stream(stream))
+    if _native is None:
+        load()
+    st = _native.prefill_ext(out, q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale,
+                             max_q_len, k_scales, v_scales, softcap, window, alibi_slopes,
+                             prefix_lens, out_lse, _handle(stream))
     _check("paged_attn_prefill_chunk_ext", st)
 
 

@@ -1,8 +1,10 @@
 """Build libpkv.so in-tree for sm_103a with nvcc.
 
 Each translation unit of csrc/ compiles in parallel to an object file under
-_build/<machine>/, then nvcc links the shared library next to this file. A
-rebuild happens only when a source or header is newer than the library.
+_build/<machine>/, then nvcc links the shared library next to this file. The
+_native module beside it (csrc/native.cpp, argument marshalling against torch's
+headers) compiles with the host compiler. A rebuild happens only when a source
+or header is newer than the library.
 """
 from __future__ import annotations
 
@@ -12,11 +14,14 @@ import os
 import platform
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpkv.so")
+NATIVE_SRC = os.path.join(CSRC, "native.cpp")
+NATIVE = os.path.join(HERE, "_native.so")
 OBJ_DIR = os.path.join(HERE, "_build", platform.machine())
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -40,14 +45,34 @@ def sources():
 
 def _deps():
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + [os.path.join(ROOT, "include", "pkv.h"), os.path.abspath(__file__)])
+            + [NATIVE_SRC, os.path.join(ROOT, "include", "pkv.h"), os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _build_native() -> None:
+    """Compile and link the _native module against the installed torch."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(root, "lib")
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f"-I{d}" for d in include], NATIVE_SRC, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {NATIVE_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
@@ -71,8 +96,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
             print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(16, os.cpu_count() or 1))) as ex:
+        native = ex.submit(_build_native)
         objs = list(ex.map(compile_one, sources()))
+        native.result()
     tmp = out + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -109,3 +109,22 @@ def test_old_calls_refuse_block_scales(lib):
                                  64, 128, 0.1, FAKE, FAKE, 0, None, FAKE, 1 << 30, None) == UNSUPPORTED
     assert lib.reshape_and_cache(FAKE, FAKE, BF16, FAKE, FAKE, BLOCK, FAKE, 4, 2, 128, 16, 8, FAKE,
                                  FAKE, None) == UNSUPPORTED
+
+
+def test_native_refuses_host_tensors(lib):
+    import torch
+    q = torch.zeros(1, 8, 128, dtype=torch.bfloat16)
+    c = torch.zeros(2, 2, 16, 128, dtype=torch.uint8)
+    s = torch.zeros(2, 2, dtype=torch.uint8)
+    t, n = torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    cu = torch.tensor([0, 1], dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        P.paged_attn_decode_ext(q, q, c, c, t, n, 0.1, 16, s, s, workspace=s)
+    with pytest.raises(ValueError, match="CUDA"):
+        P.paged_attn_prefill_chunk_ext(q, q, c, c, t, n, cu, 0.1, 1, s, s)
+    with pytest.raises(ValueError, match="CUDA"):
+        P.rope_append_block_scaled(q[:, :2], q[:, :2], c, c, s, s, t, n, cu)
+    with pytest.raises(ValueError, match="dimensions"):
+        P.paged_attn_prefill_chunk_ext(q, q[0], c, c, t, n, cu, 0.1, 1, s, s)
+    with pytest.raises(ValueError, match="tensor"):
+        P.paged_attn_prefill_chunk_ext(q, 5, c, c, t, n, cu, 0.1, 1, s, s)
