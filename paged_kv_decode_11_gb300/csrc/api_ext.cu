@@ -12,7 +12,7 @@
 #pragma GCC visibility pop
 #include "host.h"
 #include "launch_ext.h"
-#include "plan.h"
+#include "plan_ext.h"
 
 using namespace pkv;
 
@@ -71,9 +71,14 @@ extern "C" {
 size_t paged_attn_decode_ext_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
                                             int head_dim, int max_seq_len, int window,
                                             int partition_tokens) {
-  if (window < 0 || max_seq_len < 0) return 0;
-  return paged_attn_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                          plan_span(max_seq_len, window), partition_tokens);
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      max_seq_len < 0 || window < 0 || partition_tokens < 0 || partition_tokens % 16 != 0 ||
+      partition_tokens > kMaxPartitionTokens)
+    return 0;
+  // E4M3 caches have the most resident CTAs, hence the most partitions: enough for any
+  return plan_decode_ext(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                         plan_span(max_seq_len, window), partition_tokens, true, sm_count())
+      .bytes;
 }
 
 pkv_status paged_attn_decode_ext(void* out, const void* q, pkv_dtype q_dtype, const void* k_cache,
@@ -97,13 +102,13 @@ pkv_status paged_attn_decode_ext(void* out, const void* q, pkv_dtype q_dtype, co
 
   const int sms = sm_count();
   const int span = plan_span(max_seq_len, window);
-  const DecodePlan pl = plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, span,
-                                    partition_tokens, sms);
+  const bool block_scaled = kv_dtype == PKV_FP8_E4M3_BLOCK;
+  const pkv_dtype page_dtype = block_scaled ? PKV_FP8_E4M3 : kv_dtype;
+  const DecodePlan pl = plan_decode_ext(num_seqs, num_q_heads, num_kv_heads, head_dim, span,
+                                        partition_tokens, page_dtype == PKV_FP8_E4M3, sms);
   if (workspace == nullptr || workspace_bytes < pl.bytes ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PKV_ERR_WORKSPACE;
-  const bool block_scaled = kv_dtype == PKV_FP8_E4M3_BLOCK;
-  const pkv_dtype page_dtype = block_scaled ? PKV_FP8_E4M3 : kv_dtype;
   const int shift = page_shift(block_size), bs_log2 = block_log2(block_size);
   CUtensorMap tmK, tmV;
   if (!make_kv_tmap(&tmK, k_cache, page_dtype, head_dim, num_kv_heads, num_blocks, shift) ||

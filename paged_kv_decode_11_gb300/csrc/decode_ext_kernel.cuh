@@ -419,19 +419,27 @@ __global__ void __launch_bounds__(NW * 32)
   __syncthreads();
   if (!s_last) return;
   if (tid == 0) *ctr = 0ull;
+  // A chunk of CH partitions comes into the ring's space in one bulk copy per
+  // head. Then a warp per head turns the chunk's log2-sum-exps into weights
+  // 2^(lse - M) against the running maximum M (and says by how much to scale what
+  // was summed before), and every thread sums its float4 columns with them: no
+  // exponential and no branch in that loop. (With both in it a partition took
+  // 0.17 us, and contexts could not be split finely.)
   constexpr int NF = (NH * (D / 4) + NTH - 1) / NTH;   // float4 columns per thread
   constexpr int AVAIL = Cfg::SMEM_BYTES - 1024;         // the ring's space
   const int CH = max(1, min(nparts, (AVAIL - 16) / (G * (D + 1) * 4)));
-  float* s_lse = reinterpret_cast<float*>(basep);                       // [G][CH]
+  float* s_w = reinterpret_cast<float*>(basep);                         // [G][CH]
   float* s_o = reinterpret_cast<float*>(basep + ((G * CH * 4 + 15) & ~15));  // [G][CH][D]
-  float M[NF], Z[NF];
+  __shared__ float s_scale[NH];
+  float M[(NH + NW - 1) / NW], Z[(NH + NW - 1) / NW];  // of the warp's heads warp, warp + NW, ..
   float4 acc[NF];
 #pragma unroll
-  for (int i = 0; i < NF; ++i) {
+  for (int i = 0; i < (NH + NW - 1) / NW; ++i) {
     M[i] = -INFINITY;
     Z[i] = 0.f;
-    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+#pragma unroll
+  for (int i = 0; i < NF; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   const float* lse_rows = p.ws_lse + row0 * (int64_t)p.max_parts;
   for (int c0 = 0, ci = 0; c0 < nparts; c0 += CH, ++ci) {
     const int n = min(CH, nparts - c0);
@@ -442,11 +450,35 @@ __global__ void __launch_bounds__(NW * 32)
         bulk_load(s_o + hh * CH * D, p.ws_o + ((row0 + hh) * p.max_parts + c0) * D,
                   (uint32_t)(n * D * 4), &s_mbar);
     }
-#pragma unroll 4
-    for (int i = tid; i < G * n; i += NTH) {
-      const int hh = i / n, sp = i - hh * n;
-      s_lse[hh * CH + sp] = ldcg_f32(lse_rows + hh * p.max_parts + c0 + sp);
+#pragma unroll
+    for (int i = 0; i < (NH + NW - 1) / NW; ++i) {
+      const int hh = warp + NW * i;
+      if (hh >= G) continue;
+      float top = M[i];
+      for (int sp = lane; sp < n; sp += 32) {
+        const float v = ldcg_f32(lse_rows + hh * p.max_parts + c0 + sp);
+        s_w[hh * CH + sp] = v;
+        top = fmaxf(top, v);
+      }
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      for (int sp = lane; sp < n; sp += 32) {          // each lane its own values
+        const float w = exp2f(s_w[hh * CH + sp] - ref);
+        s_w[hh * CH + sp] = w;
+        sum += w;
+      }
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      const float scale = M[i] == -INFINITY ? 0.f : exp2f(M[i] - ref);
+      Z[i] = Z[i] * scale + sum;
+      M[i] = top;
+      if (lane == 0) s_scale[hh] = scale;
     }
+    // the vote is also the barrier that publishes the weights; a CTA whose
+    // copies did not all land leaves as one, after waiting once more
+    // (bounded), since they target its own shared memory
     const bool landed = mbar_wait_bounded(&s_mbar, ci & 1);
     if (__syncthreads_or(!landed)) {
       if (tid == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
@@ -458,35 +490,41 @@ __global__ void __launch_bounds__(NW * 32)
       const int f = tid + i * NTH;
       if (f < G * (D / 4)) {
         const int hh = f / (D / 4), d4 = f - hh * (D / 4);
+        const float sc = s_scale[hh];
+        acc[i].x *= sc; acc[i].y *= sc; acc[i].z *= sc; acc[i].w *= sc;
+        const float* w = s_w + hh * CH;
+        const float4* o = reinterpret_cast<const float4*>(s_o + hh * CH * D) + d4;
+#pragma unroll 4
         for (int sp = 0; sp < n; ++sp) {
-          const float ls = s_lse[hh * CH + sp];
-          if (ls == -INFINITY) continue;
-          if (ls > M[i]) {
-            const float sc = M[i] == -INFINITY ? 0.f : exp2f(M[i] - ls);
-            acc[i].x *= sc; acc[i].y *= sc; acc[i].z *= sc; acc[i].w *= sc;
-            Z[i] *= sc;
-            M[i] = ls;
-          }
-          const float w = exp2f(ls - M[i]);
-          const float4 v = *reinterpret_cast<const float4*>(s_o + (hh * CH + sp) * D + d4 * 4);
-          Z[i] += w;
-          acc[i].x += w * v.x; acc[i].y += w * v.y; acc[i].z += w * v.z; acc[i].w += w * v.w;
+          const float4 v = o[sp * (D / 4)];
+          acc[i].x = fmaf(w[sp], v.x, acc[i].x);
+          acc[i].y = fmaf(w[sp], v.y, acc[i].y);
+          acc[i].z = fmaf(w[sp], v.z, acc[i].z);
+          acc[i].w = fmaf(w[sp], v.w, acc[i].w);
         }
       }
     }
     __syncthreads();   // the next chunk reuses the staging space
   }
 #pragma unroll
+  for (int i = 0; i < (NH + NW - 1) / NW; ++i) {
+    const int hh = warp + NW * i;
+    if (hh >= G || lane != 0) continue;
+    // (a NaN sum stays one)
+    s_scale[hh] = Z[i] == 0.f ? 0.f : vscale / Z[i];
+    if (p.out_lse != nullptr)
+      p.out_lse[row0 + hh] = Z[i] == 0.f ? -INFINITY : (M[i] + log2f(Z[i])) * kLn2;
+  }
+  __syncthreads();
+#pragma unroll
   for (int i = 0; i < NF; ++i) {
     const int f = tid + i * NTH;
     if (f < G * (D / 4)) {
       const int hh = f / (D / 4), d4 = f - hh * (D / 4);
-      const float inv = Z[i] > 0.f ? vscale / Z[i] : 0.f;
+      const float inv = s_scale[hh];
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (row0 + hh) * D + d4 * 4) =
           make_uint2(pack2<QBF16>(acc[i].x * inv, acc[i].y * inv),
                      pack2<QBF16>(acc[i].z * inv, acc[i].w * inv));
-      if (d4 == 0 && p.out_lse != nullptr)
-        p.out_lse[row0 + hh] = Z[i] > 0.f ? (M[i] + log2f(Z[i])) * kLn2 : -INFINITY;
     }
   }
 }

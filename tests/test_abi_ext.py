@@ -61,6 +61,25 @@ def test_decode_ext_workspace(lib):
     assert size(4, 8, 2, 128, -1, 0, 64) == 0
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 8, 8), (128, 32, 8), (256, 16, 2)])
+def test_decode_ext_workspace_is_that_of_the_type_with_most_parts(lib, D, Hq, Hkv):
+    # the size is that of the type with the most partitions, and one byte less is refused for it
+    # (calls that would pass the check are made where there are real buffers)
+    for B in (1, 3, 17, 200):
+        for msl in (1, 15, 700, 4096, 131072):
+            for win in (0, 1, 300, 5000):
+                need = P.paged_attn_decode_ext_workspace_size(B, Hq, Hkv, D, msl, win)
+                span = min(msl, win + 15) if win else msl
+                # room for the output rows of every partition, at least 64 keys each
+                assert need >= B * Hkv * 8 + B * Hq * (4 * D + 4)
+                assert need <= 768 + B * Hkv * 8 + B * Hq * (4 * D + 4) * (span // 64 + 1)
+                a = dict(B=B, Hq=Hq, Hkv=Hkv, D=D, msl=msl, win=win, ws=FAKE)
+                for kv in (BF16, FP8, BLOCK):
+                    assert _decode(lib, **a, kv_dtype=kv, wsb=255) == WORKSPACE
+                assert _decode(lib, **a, kv_dtype=BLOCK, wsb=need - 1) == WORKSPACE
+                assert _decode(lib, **a, kv_dtype=FP8, wsb=need - 1) == WORKSPACE
+
+
 def _prefill(lib, **kw):
     a = dict(out=FAKE, q=FAKE, q_dtype=BF16, k=FAKE, v=FAKE, kv_dtype=BLOCK, bt=FAKE, sl=FAKE,
              cu=FAKE, n=1, T=10, maxq=10, Hq=8, Hkv=2, D=128, BS=16, maxb=8, nb=64, scale=0.1,
