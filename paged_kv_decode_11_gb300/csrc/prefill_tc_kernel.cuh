@@ -50,8 +50,8 @@
 //   kTcModScores: cap, bias by distance, window and prefix. The keys start at
 //   the page of the first key any row of the tile sees, and every score is
 //   rewritten once, in registers, between tensor memory and the maximum.
-// Both take 64-key tiles, which keep a row's scores in registers from the
-// maximum to P.
+// Both take the 128-key tiles (up to D = 128); a rewritten score goes back to
+// tensor memory if it does not stay in registers until P.
 #pragma once
 #include <cuda.h>
 #include <type_traits>
@@ -79,11 +79,14 @@ constexpr int kTcPlain = 0, kTcBlockScales = 1, kTcModScores = 2;   // MODE bits
 // of f16) into the rings the MMAs read.
 // ALONE: nothing else runs on the GPU beside this grid (a chunk call of its
 // own, not the prefill half of a varlen step).
-template <int D, int NST, bool KV8 = false, bool ALONE = true>
+// The MODE kernels run alone and take the 128-key tiles with E4M3 caches too: there
+// the producers of an operand split a tile by pages, each staging and converting
+// its own. (One converting warp per operand held the 64-key tiles to 1.7 us each.)
+template <int D, int NST, bool KV8 = false, bool ALONE = true, int MODE = kTcPlain>
 struct PrefillTcCfg {
   // 128-key tiles (WIDE): one softmax group over two S buffers in tensor
   // memory, P written over its own S; otherwise two groups up to D = 128
-  static constexpr bool WIDE = ALONE && !KV8 && D <= 128;
+  static constexpr bool WIDE = D <= 128 && (MODE != kTcPlain || (ALONE && !KV8));
   static constexpr int NG = WIDE ? 1 : (D <= 128 ? 2 : 1);
   // keys per tile (the S MMA's N): 128 for 16-bit caches at D <= 128 running
   // alone, with one S buffer (TMEM) and one P buffer (shared) per group; 64
@@ -123,7 +126,7 @@ struct PrefillTcCfg {
   static constexpr int RING_BYTES = NST * KV_BYTES;          // one ring (K, then V)
   static constexpr int P_CB = kTcRows * 128;                 // 64 keys of a P buffer
   static constexpr int P_BYTES = (KEYS / 64) * P_CB;         // one P buffer (NSB per group)
-  static constexpr int NSS = KV8 ? 4 : 0;                    // staging stages per operand
+  static constexpr int NSS = KV8 ? (WIDE ? 2 : 4) : 0;       // staging stages per operand
   static constexpr int STG_PAGE = kBS * D;                   // one E4M3 page
   static constexpr int STG_BYTES = PAGES * STG_PAGE;         // one staged E4M3 tile
   static constexpr int SMEM_BYTES =
@@ -219,7 +222,7 @@ __host__ __device__ __forceinline__ const PrefillParams& prefill_base(const Pref
 // ones otherwise (an E4M3 cache is converted to f16, and bf16 queries with
 // it). QBF16: the query and output type.
 template <int D, int KV, bool QBF16, int NST, int SPLIT, bool ALONE, int MODE>
-__global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::THREADS, 1)
+__global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MODE>::THREADS, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV,
@@ -229,14 +232,15 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::TH
   static_assert(!BSC || KV == KV_E4M3, "block scales are for E4M3 codes");
   constexpr bool KV8 = KV == KV_E4M3;
   constexpr bool BF16 = KV == KV_BF16;                  // MMA operand type
-  using Cfg = PrefillTcCfg<D, NST, KV8, ALONE>;
+  using Cfg = PrefillTcCfg<D, NST, KV8, ALONE, MODE>;
   constexpr int NG = Cfg::NG;
   constexpr int NSS = Cfg::NSS > 0 ? Cfg::NSS : 1;
   constexpr int kTcKeys = Cfg::KEYS, kTcPages = Cfg::PAGES, NSB = Cfg::NSB;
   extern __shared__ uint8_t smem_raw[];
   // per ring stage: K (or V) tile ready, K (or V) tile read
   __shared__ uint64_t full_k[NST], empty_k[NST], full_v[NST], empty_v[NST];
-  __shared__ uint64_t stg_k[NSS], stg_v[NSS];           // KV8: staged E4M3 tile landed
+  // KV8: staged E4M3 tile landed (its pages of one producer)
+  __shared__ uint64_t stg_k[NSS * Cfg::PK], stg_v[NSS * Cfg::PV];
   // per softmax group g and buffer b: S ready, P written, P.V done
   __shared__ uint64_t s_bar[NG][NSB], o_bar[NG][NSB], p_bar[NG][NSB];
   __shared__ uint64_t ready_bar, recv_bar;              // cluster hand-off (SPLIT == 2)
@@ -352,10 +356,11 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::TH
     const int pg0 = t * kTcPages;
     const int npg = min(kTcPages, n_pages - pg0);
     if constexpr (KV8) {
-      uint64_t* bar = &stg_x[u % NSS];
-      if (lane == 0) mbar_arrive_expect_tx(bar, npg * Cfg::STG_PAGE);
+      uint64_t* bar = &stg_x[(u % NSS) * np + pw];
+      const int mine = pw < npg ? (npg - pw + np - 1) / np : 0;
+      if (lane == 0) mbar_arrive_expect_tx(bar, mine * Cfg::STG_PAGE);
       uint8_t* dst = stage_x + (u % NSS) * Cfg::STG_BYTES;
-      for (int pg = 0; pg < npg; ++pg) {
+      for (int pg = pw; pg < npg; pg += np) {
         const int z = __shfl_sync(0xffffffffu, z_cur, (u * kTcPages + pg) % 32);
         if (lane == 0) tma_load_3d(dst + pg * Cfg::STG_PAGE, tmap, bar, 0, 0, z);
       }
@@ -373,13 +378,13 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::TH
       }
     }
   };
-  // KV8: the warp turns staged tile u into f16 in ring stage u % NST (rows
-  // past the loaded keys become zeros), then refills the staging stage
+  // KV8: the warp turns its pages of staged tile u into f16 in ring stage u % NST
+  // (rows past the loaded keys become zeros), then refills the staging stage
   auto convert = [&](int u) {
     using Geo8 = PageGeom<D, KV_E4M3>;
     constexpr int CPR = D / 16;                          // 16-element chunks per row
     const int t = t_begin + u, st = u % NST;
-    wait(&stg_x[u % NSS], (u / NSS) & 1);
+    wait(&stg_x[(u % NSS) * np + pw], (u / NSS) & 1);
     if (u >= NST) wait(&empty_x[st], ((u / NST) - 1) & 1);
     const uint8_t* src = stage_x + (u % NSS) * Cfg::STG_BYTES;
     const int valid = loaded_end - t * kTcKeys;          // rows of this tile holding keys
@@ -389,22 +394,51 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::TH
     const int x = lane % CPR, rsub = lane / CPR;
     uint8_t* dcol = ring_x + st * Cfg::KV_BYTES + (x / 4) * Cfg::KV_BOX;
     const int c16 = 2 * (x % 4);
+    if constexpr (Cfg::WIDE) {
+      // this producer's pages one by one, a page's reads ahead of its stores; a
+      // loop, not unrolled further: with a tile's worth of straight-line code here
+      // the softmax warps waited for instructions (7,000 cycles a tile, not 2,100)
+#pragma unroll 1
+      for (int pg = pw; pg < kTcPages; pg += np) {
+        uint4 e[kBS / RPI];
 #pragma unroll
-    for (int k = 0; k < kTcKeys / RPI; ++k) {
-      const int row = k * RPI + rsub;
-      // rows of pages not loaded hold stale bytes: read anyway, zero below
-      const uint4 e = *reinterpret_cast<const uint4*>(src + (row / kBS) * Cfg::STG_PAGE +
-                                                      Geo8::row_off(row % kBS, 16 * x));
-      const bool keep = row < valid && (!MOD || t > 0 || row >= head);
-      const uint4 lo = keep ? make_uint4(e4m3x2_to_f16x2(e.x & 0xFFFFu), e4m3x2_to_f16x2(e.x >> 16),
-                                         e4m3x2_to_f16x2(e.y & 0xFFFFu), e4m3x2_to_f16x2(e.y >> 16))
-                            : make_uint4(0u, 0u, 0u, 0u);
-      const uint4 hi = keep ? make_uint4(e4m3x2_to_f16x2(e.z & 0xFFFFu), e4m3x2_to_f16x2(e.z >> 16),
-                                         e4m3x2_to_f16x2(e.w & 0xFFFFu), e4m3x2_to_f16x2(e.w >> 16))
-                            : make_uint4(0u, 0u, 0u, 0u);
-      // elements 16 x .. 16 x + 15: 16-byte chunks c16 and c16 + 1 of the row
-      *reinterpret_cast<uint4*>(dcol + swz128(row, c16)) = lo;
-      *reinterpret_cast<uint4*>(dcol + swz128(row, c16 + 1)) = hi;
+        for (int k = 0; k < kBS / RPI; ++k) {
+          const int row = pg * kBS + k * RPI + rsub;
+          // rows of pages not loaded hold stale bytes: read anyway, zeroed here
+          e[k] = *reinterpret_cast<const uint4*>(src + pg * Cfg::STG_PAGE +
+                                                 Geo8::row_off(k * RPI + rsub, 16 * x));
+          const uint32_t m = row < valid && (!MOD || t > 0 || row >= head) ? 0xFFFFFFFFu : 0u;
+          e[k] = make_uint4(e[k].x & m, e[k].y & m, e[k].z & m, e[k].w & m);
+        }
+#pragma unroll
+        for (int k = 0; k < kBS / RPI; ++k) {
+          const int row = pg * kBS + k * RPI + rsub;
+          *reinterpret_cast<uint4*>(dcol + swz128(row, c16)) =
+              make_uint4(e4m3x2_to_f16x2(e[k].x & 0xFFFFu), e4m3x2_to_f16x2(e[k].x >> 16),
+                         e4m3x2_to_f16x2(e[k].y & 0xFFFFu), e4m3x2_to_f16x2(e[k].y >> 16));
+          *reinterpret_cast<uint4*>(dcol + swz128(row, c16 + 1)) =
+              make_uint4(e4m3x2_to_f16x2(e[k].z & 0xFFFFu), e4m3x2_to_f16x2(e[k].z >> 16),
+                         e4m3x2_to_f16x2(e[k].w & 0xFFFFu), e4m3x2_to_f16x2(e[k].w >> 16));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kTcKeys / RPI; ++k) {
+        const int row = k * RPI + rsub;
+        // rows of pages not loaded hold stale bytes: read anyway, zero below
+        const uint4 e = *reinterpret_cast<const uint4*>(src + (row / kBS) * Cfg::STG_PAGE +
+                                                        Geo8::row_off(row % kBS, 16 * x));
+        const bool keep = row < valid;
+        const uint4 lo = keep ? make_uint4(e4m3x2_to_f16x2(e.x & 0xFFFFu), e4m3x2_to_f16x2(e.x >> 16),
+                                           e4m3x2_to_f16x2(e.y & 0xFFFFu), e4m3x2_to_f16x2(e.y >> 16))
+                              : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 hi = keep ? make_uint4(e4m3x2_to_f16x2(e.z & 0xFFFFu), e4m3x2_to_f16x2(e.z >> 16),
+                                           e4m3x2_to_f16x2(e.w & 0xFFFFu), e4m3x2_to_f16x2(e.w >> 16))
+                              : make_uint4(0u, 0u, 0u, 0u);
+        // elements 16 x .. 16 x + 15: 16-byte chunks c16 and c16 + 1 of the row
+        *reinterpret_cast<uint4*>(dcol + swz128(row, c16)) = lo;
+        *reinterpret_cast<uint4*>(dcol + swz128(row, c16 + 1)) = hi;
+      }
     }
     fence_proxy_async_smem();                            // the tensor cores read these stores
     mbar_arrive(&full_x[st]);                            // one arrival per lane
@@ -420,15 +454,13 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::TH
       prefetch_tensormap(&tmK);
       prefetch_tensormap(&tmV);
       for (int s = 0; s < NST; ++s) {
-        mbar_init(&full_k[s], KV8 ? 32 : Cfg::PK);      // KV8: the converting warp's lanes
+        mbar_init(&full_k[s], KV8 ? 32 * Cfg::PK : Cfg::PK);   // KV8: the converting lanes
         mbar_init(&empty_k[s], 1);
-        mbar_init(&full_v[s], KV8 ? 32 : Cfg::PV);
+        mbar_init(&full_v[s], KV8 ? 32 * Cfg::PV : Cfg::PV);
         mbar_init(&empty_v[s], 1);
       }
-      for (int s = 0; s < NSS; ++s) {
-        mbar_init(&stg_k[s], 1);
-        mbar_init(&stg_v[s], 1);
-      }
+      for (int s = 0; s < NSS * Cfg::PK; ++s) mbar_init(&stg_k[s], 1);
+      for (int s = 0; s < NSS * Cfg::PV; ++s) mbar_init(&stg_v[s], 1);
       for (int g = 0; g < NG; ++g)
         for (int b = 0; b < NSB; ++b) {
           mbar_init(&s_bar[g][b], 1);
@@ -455,7 +487,8 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::TH
     z_next = page_row(pg_begin + 32 + lane);
   }
   if constexpr (KV8) {
-    if (warp == Cfg::W_K)
+    if (Cfg::PK > 1 && k_warp) named_barrier(2, Cfg::PK * 32);   // the barriers are set up
+    if (k_warp)
       for (int u = 0; u < Cfg::NSS && u < n_tiles; ++u) issue(u);
   } else if (producer) {
     // the first S product needs only the query tile and K tile 0: the K
@@ -693,25 +726,31 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::TH
     // tile is read from TMEM twice, for the max and then for P, which keeps
     // 64 scores in registers
     constexpr int HALVES = kTcKeys / 64;
-    static_assert(MODE == kTcPlain || HALVES == 1, "a row's scores stay in registers");
-    // BSC: the pages' score factors and V exponents
-    float kf[kTcPages], ev[kTcPages];
+    // (MODE: the code of a half once, for the instruction caches' sake)
+    constexpr int kUnrollHalves = MODE == kTcPlain ? HALVES : 1;
+    // BSC: the score factors and V exponents of the four pages of a 64-key half
+    float kf[4], ev[4];
     if constexpr (BSC) {
       if ((u * kTcPages) / 32 != sc_chunk) {
         sc_cur = sc_next;
         sc_next = scales_of(++sc_chunk + 1);
       }
-#pragma unroll
-      for (int pg = 0; pg < kTcPages; ++pg) {
-        const uint32_t sc = __shfl_sync(0xffffffffu, sc_cur, (u * kTcPages + pg) % 32);
-        // (not below the least normal number, so that a masked -inf stays -inf)
-        const float f = sl2 * e8m0_value(sc & 0xFFu);
-        kf[pg] = f < 0x1p-126f ? 0x1p-126f : f;
-        ev[pg] = e8m0_log2(sc >> 8);
-      }
     }
+    auto load_scales = [&](int hh) {
+      if constexpr (BSC) {
+#pragma unroll
+        for (int pg = 0; pg < 4; ++pg) {
+          const uint32_t sc =
+              __shfl_sync(0xffffffffu, sc_cur, (u * kTcPages + 4 * hh + pg) % 32);
+          // (not below the least normal number, so that a masked -inf stays -inf)
+          const float f = sl2 * e8m0_value(sc & 0xFFu);
+          kf[pg] = f < 0x1p-126f ? 0x1p-126f : f;
+          ev[pg] = e8m0_log2(sc >> 8);
+        }
+      }
+    };
     float x[64];
-    auto load_half = [&](int hh) {
+    auto load_half = [&](int hh, bool first_time) {
       uint32_t sv[2][32];
       tc::ld32(sbuf + hh * 64, sv[0]);
       tc::ld32(sbuf + hh * 64 + 32, sv[1]);
@@ -719,7 +758,7 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::TH
 #pragma unroll
       for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(sv[c / 32][c % 32]);
       const int k0 = t * kTcKeys + hh * 64;
-      if constexpr (MOD) {
+      if constexpr (MOD) if (first_time) {
         // the scores themselves, in log2 units
 #pragma unroll
         for (int c = 0; c < 64; ++c) x[c] *= BSC ? kf[c / kBS] : sl2;
@@ -738,40 +777,54 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::TH
           }
         }
       }
-      if (k0 + 63 > last) {
+      if ((!MOD || first_time) && k0 + 63 > last) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
           if (k0 + c > last) x[c] = -INFINITY;
       }
-      if (MOD && k0 < lo) {
+      if (MOD && first_time && k0 < lo) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
           if (k0 + c < lo) x[c] = -INFINITY;
       }
+      // MOD: back where they came from, unless they stay in registers until P
+      if (MOD && first_time && hh < HALVES - 1) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t v[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(x[32 * w + c]);
+          tc::st32(sbuf + hh * 64 + 32 * w, v);
+        }
+        tc::wait_st();
+      }
     };
     float mx, mxw = -INFINITY;                          // largest score; BSC: largest score + ev
     if constexpr (BSC) {
-      load_half(0);
-      // two chains per page
-      float pm[kTcPages][2];
-#pragma unroll
-      for (int c = 0; c < 64; ++c)
-        pm[c / kBS][c % 2] = c % kBS < 2 ? x[c] : fmaxf(pm[c / kBS][c % 2], x[c]);
       mx = -INFINITY;
+#pragma unroll 1
+      for (int hh = 0; hh < HALVES; ++hh) {
+        load_scales(hh);
+        load_half(hh, true);
+        float pm[4][2];                                 // two chains per page
 #pragma unroll
-      for (int pg = 0; pg < kTcPages; ++pg) {
-        const float top = fmaxf(pm[pg][0], pm[pg][1]) * (MOD ? 1.f : kf[pg]);
-        mx = fmaxf(mx, top);
-        mxw = fmaxf(mxw, top + ev[pg]);
+        for (int c = 0; c < 64; ++c)
+          pm[c / kBS][c % 2] = c % kBS < 2 ? x[c] : fmaxf(pm[c / kBS][c % 2], x[c]);
+#pragma unroll
+        for (int pg = 0; pg < 4; ++pg) {
+          const float top = fmaxf(pm[pg][0], pm[pg][1]) * (MOD ? 1.f : kf[pg]);
+          mx = fmaxf(mx, top);
+          mxw = fmaxf(mxw, top + ev[pg]);
+        }
       }
     } else {
       // row max over 8 independent chains, then a tree
       float m8[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) m8[k] = -INFINITY;
-#pragma unroll
+#pragma unroll kUnrollHalves
       for (int hh = 0; hh < HALVES; ++hh) {
-        load_half(hh);
+        load_half(hh, true);
 #pragma unroll
         for (int c = 0; c < 64; ++c) m8[c % 8] = fmaxf(m8[c % 8], x[c]);
       }
@@ -810,35 +863,52 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::TH
     }
     // P buffer b was read by the P.V of this group's tile j - NSB
     if (j >= NSB) wait(&o_bar[grp][b], ((j - NSB) / NSB) & 1);
-    const float ms = o_ref == -INFINITY ? 0.f : o_ref;
+    const float ms = m_ref == -INFINITY ? 0.f : m_ref;
     uint8_t* pPb = pP + (NSB * grp + b) * Cfg::P_BYTES;
     float rs8[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) rs8[k] = 0.f;
-#pragma unroll
+#pragma unroll kUnrollHalves
     for (int it = 0; it < HALVES; ++it) {
       // PTM: the last half first, from the registers the max pass left it in,
       // then the others reloaded; P of keys 64 hh .. 64 hh + 63 goes to
       // columns 64 hh .. 64 hh + 31, the first half of that half's own scores
       // (already in x), so no score is overwritten before it is read
       const int hh = Cfg::PTM ? HALVES - 1 - it : it;
-      if (HALVES > 1 && (!Cfg::PTM || it > 0)) load_half(hh);   // (else x holds it)
+      if (HALVES > 1 && (!Cfg::PTM || it > 0)) {
+        load_scales(hh);
+        load_half(hh, false);
+      }                                                 // (else x, kf and ev hold it)
       uint32_t pv[32];
+      // BSC: P of page pg is its probabilities times 2^-back, back = w_ref - ev -
+      // m_ref: relative to O's reference, with the page's V scale in it. A page
+      // whose V scale is so small that its P would leave fp32 (back above 80: its
+      // part of O is nothing) keeps a P of 2^-80 times the probabilities, 0 in
+      // f16, so that its sum stays exact.
+      float ps[4], back[4];
+      if constexpr (BSC) {
+        const float wr = w_ref == -INFINITY ? 0.f : w_ref;
+#pragma unroll
+        for (int pg = 0; pg < 4; ++pg) {
+          const float d = wr - ev[pg] - ms;
+          back[pg] = d > 80.f ? 80.f : d;
+        }
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         float e[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if constexpr (BSC)                             // one page: 8 c / 16
-            e[k] = MOD ? ex2_approx(x[8 * c + k] + (ev[c / 2] - ms))
-                       : ex2_approx(fmaf(x[8 * c + k], kf[c / 2], ev[c / 2] - ms));
+            e[k] = MOD ? ex2_approx(x[8 * c + k] - (ms + back[c / 2]))
+                       : ex2_approx(fmaf(x[8 * c + k], kf[c / 2], -(ms + back[c / 2])));
           else
             e[k] = MOD ? ex2_approx(x[8 * c + k] - ms) : ex2_approx(fmaf(x[8 * c + k], sl2, -ms));
           if constexpr (!BSC) rs8[k] += e[k];
         }
-        // BSC: rs8[pg] is page pg's sum of P
+        // BSC: page c / 2 of the half's sum of P
         if constexpr (BSC)
-          rs8[c / 2] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+          ps[c / 2] = (c % 2 ? ps[c / 2] : 0.f) + ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
         const uint4 w = make_uint4(pack16x2<BF16>(e[0], e[1]), pack16x2<BF16>(e[2], e[3]),
                                    pack16x2<BF16>(e[4], e[5]), pack16x2<BF16>(e[6], e[7]));
         if constexpr (Cfg::PTM) {
@@ -851,33 +921,17 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE>::TH
         }
       }
       if constexpr (Cfg::PTM) tc::st32(sbuf + hh * 64, pv);
+      if constexpr (BSC) {
+#pragma unroll
+        for (int pg = 0; pg < 4; ++pg) rs8[pg] = fmaf(ps[pg], ex2_approx(back[pg]), rs8[pg]);
+      }
     }
     if constexpr (Cfg::PTM) tc::wait_st();
-    if constexpr (BSC) {
-      // a page's probabilities are its P times 2^(w_ref - ev - m_ref). Where that
-      // factor is so large that P's own underflow could show in the sum (V scales
-      // of one row some 2^80 apart), they are computed anew
-      const float mp = m_ref == -INFINITY ? 0.f : m_ref;
-      float sum = 0.f;
 #pragma unroll
-      for (int pg = 0; pg < kTcPages; ++pg) {
-        const float back = ms - ev[pg] - mp;
-        if (back > 80.f) {
+    for (int w = 4; w > 0; w >>= 1)
 #pragma unroll
-          for (int c = 0; c < kBS; ++c)
-            sum += ex2_approx(MOD ? x[kBS * pg + c] - mp : fmaf(x[kBS * pg + c], kf[pg], -mp));
-        } else {
-          sum = fmaf(rs8[pg], ex2_approx(back), sum);
-        }
-      }
-      l = l * l_alpha + sum;
-    } else {
-#pragma unroll
-      for (int w = 4; w > 0; w >>= 1)
-#pragma unroll
-        for (int k = 0; k < w; ++k) rs8[k] += rs8[k + w];
-      l = l * alpha + rs8[0];
-    }
+      for (int k = 0; k < w; ++k) rs8[k] += rs8[k + w];
+    l = l * l_alpha + rs8[0];
     // V rows with no data for this tile (past the context, or pages not
     // loaded) meet weight 0 in P: zero them so their contents cannot make NaN.
     // The group's threads share the rows; the P.V waits for all of them.
@@ -1064,11 +1118,13 @@ static pkv_status launch_prefill_tc_s(const PrefillTcParams<MODE>& ep, const CUt
                                       cudaStream_t stream, int dev) {
   constexpr bool KV8 = KV == KV_E4M3;
   // ring stages: the 128-key tiles (P in tensor memory) take 3 of 32 KB at
-  // D = 128 and 6 of 16 KB at D = 64; E4M3 and D = 256 take 2, the rest 4
-  constexpr bool WIDE = PrefillTcCfg<D, 2, KV8, ALONE>::WIDE;
-  constexpr int NST = WIDE ? (D == 128 ? 3 : 6) : ((D > 128 || KV8) ? 2 : 4);
-  using Cfg = PrefillTcCfg<D, NST, KV8, ALONE>;
-  static_assert(Cfg::SMEM_BYTES + 512 <= 227 * 1024, "shared memory (dynamic + static)");
+  // D = 128 and 6 of 16 KB at D = 64, less the staging of an E4M3 cache 2 and 4;
+  // the 64-key tiles of E4M3 caches and D = 256 take 2, the rest 4
+  constexpr bool WIDE = PrefillTcCfg<D, 2, KV8, ALONE, MODE>::WIDE;
+  constexpr int NST = WIDE ? (KV8 ? (D == 128 ? 2 : 4) : D == 128 ? 3 : 6)
+                           : ((D > 128 || KV8) ? 2 : 4);
+  using Cfg = PrefillTcCfg<D, NST, KV8, ALONE, MODE>;
+  static_assert(Cfg::SMEM_BYTES + 1280 <= 227 * 1024, "shared memory (dynamic + static)");
   static_assert(SPLIT == 1 || kTcRows * (D / SPLIT) * 4 + kTcRows * 16 <= 2 * Cfg::RING_BYTES,
                 "the other CTA's rows must fit in the ring");
   auto kern = prefill_tc_kernel<D, KV, QBF16, NST, SPLIT, ALONE, MODE>;
@@ -1114,7 +1170,7 @@ static int prefill_tc_sms(int dev) {
   return n;
 }
 
-// The _ext calls (64-key tiles): one CTA per query tile when that fills at
+// The _ext calls: one CTA per query tile when that fills at
 // least half of the GPU; otherwise a cluster of two per tile, each taking half
 // of the key tiles.
 template <int D, int KV, bool QBF16, int MODE>
