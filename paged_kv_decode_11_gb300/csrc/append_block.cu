@@ -36,6 +36,7 @@
 // store (sequence, block id, scale) is what takes the time, so everything that
 // can be addressed without them is loaded first.
 #include "block_scale.cuh"
+#include "f32x2.cuh"
 #include "rope.cuh"
 #include "launch_ext.h"
 
@@ -134,34 +135,6 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float f) {
   return out;
 }
 
-// Two fp32 values in one register pair, for the packed instructions.
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pack(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack(f2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 sub2(f2 a, f2 b) {
-  f2 r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // r + rem (|rem| at most half a unit in r's last place) rounded to odd.
 __device__ __forceinline__ float round_odd(float r, float rem) {
   const uint32_t b = __float_as_uint(r);
@@ -191,16 +164,16 @@ __device__ __forceinline__ Pair8 rotate_pairs(const Pair8& in, const Angles& an)
   const float s[8] = {an.s[0].x, an.s[0].y, an.s[0].z, an.s[0].w,
                       an.s[1].x, an.s[1].y, an.s[1].z, an.s[1].w};
   float y1[8], y2[8];
-  f2 finite = pack(0.f, 0.f);
+  f2 finite = pack_f2(0.f, 0.f);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const f2 x = pack(x1[e], x2[e]), z = pack(x2[e], x1[e]);
-    const f2 cc = pack(c[e], c[e]), ss = pack(-s[e], s[e]);
+    const f2 x = pack_f2(x1[e], x2[e]), z = pack_f2(x2[e], x1[e]);
+    const f2 cc = pack_f2(c[e], c[e]), ss = pack_f2(-s[e], s[e]);
     // the rounded products by single multiplications: packed ones were merged into
     // the additions below, whose error terms then belong to another sum
     const float qa = __fmul_rn(x1[e], c[e]), qb = __fmul_rn(x2[e], c[e]);
     const float pa = __fmul_rn(x2[e], -s[e]), pb = __fmul_rn(x1[e], s[e]);
-    const f2 nq = pack(-qa, -qb), p = pack(pa, pb), np = pack(-pa, -pb);
+    const f2 nq = pack_f2(-qa, -qb), p = pack_f2(pa, pb), np = pack_f2(-pa, -pb);
     const f2 qe = fma2(x, cc, nq), pe = fma2(z, ss, np);             // what they leave
     const f2 sum = sub2(p, nq);
     const f2 bb = add2(sum, nq);
@@ -208,12 +181,12 @@ __device__ __forceinline__ Pair8 rotate_pairs(const Pair8& in, const Angles& an)
     const f2 rest = add2(err, add2(qe, pe));
     const f2 r = add2(sum, rest);
     const f2 rem = sub2(rest, sub2(r, sum));
-    finite = fma2(r, pack(0.f, 0.f), finite);
-    const float2 rr = unpack(r), mm = unpack(rem);
+    finite = fma2(r, pack_f2(0.f, 0.f), finite);
+    const float2 rr = unpack_f2(r), mm = unpack_f2(rem);
     y1[e] = round_odd(rr.x, mm.x);
     y2[e] = round_odd(rr.y, mm.y);
   }
-  const float2 f = unpack(finite);
+  const float2 f = unpack_f2(finite);
   if (!(f.x == 0.f && f.y == 0.f)) {
     // an infinity or NaN among the inputs (the error terms are NaN then)
 #pragma unroll

@@ -9,6 +9,7 @@
 #pragma once
 #include <cstdint>
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace pkv {
 
@@ -74,6 +75,40 @@ __device__ __forceinline__ float softcap_log2(float x, float cap_log2, float two
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * two_over_cap));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
   return fmaf(-2.f * cap_log2, r, cap_log2);
+}
+
+// softcap_log2 of N scores of one row, the whole warp with its rows at once.
+// Scores seldom leave (-softcap, softcap), and there tanh(y) = y P(y^2) with P of
+// degree 6 is off by less than 1.3e-7 (the Chebyshev interpolant of
+// tanh(sqrt t) / sqrt t on [0, 1], evaluated in fp32): five packed operations a
+// score, where the general form takes two of the special-function unit's, which
+// the softmax itself keeps busy. A warp with a larger score takes that one.
+template <int N>
+__device__ __forceinline__ void softcap_log2_row(float (&x)[N], float cap_log2,
+                                                 float two_over_cap) {
+  constexpr float kP[7] = {0.99999994f, -0.33332857f, 0.13325398f, -0.053465176f,
+                           0.02030552f, -0.0062170699f, 0.0010455536f};
+  const float inv = two_over_cap * (0.5f * kLn2);       // 1 / cap_log2
+  float top = 0.f;
+#pragma unroll
+  for (int c = 0; c < N; ++c) top = fmaxf(top, fabsf(x[c]));
+  if (__all_sync(0xffffffffu, top * inv <= 1.f)) {
+    const f2 i2 = pack_f2(inv, inv);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+      const f2 v = pack_f2(x[c], x[c + 1]);
+      const f2 y = mul2(v, i2), t = mul2(y, y);
+      f2 h = pack_f2(kP[6], kP[6]);
+#pragma unroll
+      for (int k = 5; k >= 0; --k) h = fma2(h, t, pack_f2(kP[k], kP[k]));
+      const float2 r = unpack_f2(mul2(v, h));
+      x[c] = r.x;
+      x[c + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c) x[c] = softcap_log2(x[c], cap_log2, two_over_cap);
+  }
 }
 
 }  // namespace pkv

@@ -50,8 +50,6 @@
 //   kTcModScores: cap, bias by distance, window and prefix. The keys start at
 //   the page of the first key any row of the tile sees, and every score is
 //   rewritten once, in registers, between tensor memory and the maximum.
-// Both take the 128-key tiles (up to D = 128); a rewritten score goes back to
-// tensor memory if it does not stay in registers until P.
 #pragma once
 #include <cuda.h>
 #include <type_traits>
@@ -79,15 +77,20 @@ constexpr int kTcPlain = 0, kTcBlockScales = 1, kTcModScores = 2;   // MODE bits
 // of f16) into the rings the MMAs read.
 // ALONE: nothing else runs on the GPU beside this grid (a chunk call of its
 // own, not the prefill half of a varlen step).
-// The MODE kernels run alone and take the 128-key tiles with E4M3 caches too: there
-// the producers of an operand split a tile by pages, each staging and converting
-// its own. (One converting warp per operand held the 64-key tiles to 1.7 us each.)
+// The MODE kernels always run alone, in 128-key tiles up to D = 128, with two
+// softmax groups over one S buffer each: their softmax has more work per key (scales
+// per page, rewritten scores), so one group's runs while the other's products do.
+// Long chunk of block scales (2,048 on 4,096, D = 128): 292 us; with one group over
+// three buffers 302, two groups over 64-key tiles 358. The producers of an E4M3
+// operand split a tile by pages (SHARE), each staging and converting its own; with
+// one converting warp per operand that chunk took 558 us.
 template <int D, int NST, bool KV8 = false, bool ALONE = true, int MODE = kTcPlain>
 struct PrefillTcCfg {
   // 128-key tiles (WIDE): one softmax group over two S buffers in tensor
   // memory, P written over its own S; otherwise two groups up to D = 128
   static constexpr bool WIDE = D <= 128 && (MODE != kTcPlain || (ALONE && !KV8));
-  static constexpr int NG = WIDE ? 1 : (D <= 128 ? 2 : 1);
+  static constexpr bool SHARE = KV8 && MODE != kTcPlain;
+  static constexpr int NG = WIDE ? (MODE == kTcPlain ? 1 : 2) : (D <= 128 ? 2 : 1);
   // keys per tile (the S MMA's N): 128 for 16-bit caches at D <= 128 running
   // alone, with one S buffer (TMEM) and one P buffer (shared) per group; 64
   // otherwise, with two. Beside a decode grid the 64-key kernel, whose loads
@@ -97,12 +100,12 @@ struct PrefillTcCfg {
   static constexpr int PAGES = KEYS / kBS;                   // 16-token pages per tile
   // S (and P) buffers per group: three for the one group of 128-key tiles
   // (3 x 128 S columns and 128 of O fill the 512), so an S product waits for
-  // the P.V two tiles back, not the one before
-  static constexpr int NSB = WIDE ? 3 : 2;
+  // the P.V two tiles back, not the one before; one for two groups (MODE)
+  static constexpr int NSB = WIDE ? (MODE == kTcPlain ? 3 : 1) : 2;
   // P in tensor memory (128-key tiles): the softmax writes P over its own S
   // columns (two 16-bit values per 32-bit column) and the P.V MMAs read it
   // there, which frees the shared P buffers for deeper K and V rings
-  static constexpr bool PTM = WIDE;
+  static constexpr bool PTM = WIDE || MODE != kTcPlain;
   static constexpr int PK = WIDE ? 4 : 1;
   static constexpr int PV = WIDE ? 3 : 1;
   static constexpr int WARPS = 4 * NG + PK + 1 + PV;
@@ -111,7 +114,7 @@ struct PrefillTcCfg {
   // 16 warps (4 per SM sub-partition) launch at 128 registers a thread: the
   // softmax warpgroups rise to REG_SOFTMAX, the K producers (warpgroup 2) and
   // the MMA warp with the V producers (warpgroup 3) fall to REG_K / REG_MV
-  static constexpr bool REALLOC = WARPS == 16;
+  static constexpr bool REALLOC = WARPS == 16 && MODE == kTcPlain;
   static constexpr int REG_SOFTMAX = 184, REG_K = 48, REG_MV = 56;
   static_assert(!REALLOC || (NG == 2 && W_MMA == 12), "warpgroups: 2 softmax, K, MMA + V");
   // registers the warpgroups hold after the moves; the launcher checks that
@@ -253,7 +256,9 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   // the SM room this grid leaves as soon as all of its CTAs are running
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int qt = blockIdx.x / SPLIT, h = blockIdx.y, n = blockIdx.z;
+  // (MODE: the last query tiles, which see the most keys, first)
+  const int qt = (MODE == kTcPlain ? blockIdx.x : gridDim.x - 1 - blockIdx.x) / SPLIT;
+  const int h = blockIdx.y, n = blockIdx.z;
   const int split = SPLIT > 1 ? (int)cluster_rank() : 0;
   const int G = p.G;
   const int q0 = p.cu_q_lens[n];
@@ -321,6 +326,15 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   // block-table read waits in front of a TMA issue; lane 0 issues the loads.
   const int pg_begin = t_begin * kTcPages;
   const int pg_end = min(n_pages, (t_begin + n_tiles) * kTcPages);
+  // The key tile of local tile u, and the page at place i of the sequence of the
+  // tiles' pages. MODE: the last tiles first, so that with a bias by distance the
+  // largest scores come first and O is not rescaled tile after tile.
+  auto tile_of = [&](int u) { return t_begin + (MODE == kTcPlain ? u : n_tiles - 1 - u); };
+  auto page_of = [&](int i) {
+    if constexpr (MODE == kTcPlain) return pg_begin + i;
+    if (i >= n_tiles * kTcPages) return pg_end;
+    return tile_of(i / kTcPages) * kTcPages + i % kTcPages;
+  };
   auto page_row = [&](int lp) -> int {
     if (lp >= pg_end) return 0;
     if constexpr (MOD) lp += origin / kBS;
@@ -347,11 +361,11 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   // TMA loads of tile u: into ring stage u % NST, or (KV8) into staging
   // stage u % NSS, one box per E4M3 page
   auto issue = [&](int u) {
-    const int t = t_begin + u;
+    const int t = tile_of(u);
     if ((u * kTcPages) / 32 != chunk) {
       z_cur = z_next;
       ++chunk;
-      z_next = page_row(pg_begin + 32 * (chunk + 1) + lane);
+      z_next = page_row(page_of(32 * (chunk + 1) + lane));
     }
     const int pg0 = t * kTcPages;
     const int npg = min(kTcPages, n_pages - pg0);
@@ -383,7 +397,7 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   auto convert = [&](int u) {
     using Geo8 = PageGeom<D, KV_E4M3>;
     constexpr int CPR = D / 16;                          // 16-element chunks per row
-    const int t = t_begin + u, st = u % NST;
+    const int t = tile_of(u), st = u % NST;
     wait(&stg_x[(u % NSS) * np + pw], (u / NSS) & 1);
     if (u >= NST) wait(&empty_x[st], ((u / NST) - 1) & 1);
     const uint8_t* src = stage_x + (u % NSS) * Cfg::STG_BYTES;
@@ -394,7 +408,8 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
     const int x = lane % CPR, rsub = lane / CPR;
     uint8_t* dcol = ring_x + st * Cfg::KV_BYTES + (x / 4) * Cfg::KV_BOX;
     const int c16 = 2 * (x % 4);
-    if constexpr (Cfg::WIDE) {
+    const int odd = x / 4;                               // (column block: 0, 1 at D = 128)
+    if constexpr (Cfg::SHARE) {
       // this producer's pages one by one, a page's reads ahead of its stores; a
       // loop, not unrolled further: with a tile's worth of straight-line code here
       // the softmax warps waited for instructions (7,000 cycles a tile, not 2,100)
@@ -413,12 +428,16 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
 #pragma unroll
         for (int k = 0; k < kBS / RPI; ++k) {
           const int row = pg * kBS + k * RPI + rsub;
-          *reinterpret_cast<uint4*>(dcol + swz128(row, c16)) =
-              make_uint4(e4m3x2_to_f16x2(e[k].x & 0xFFFFu), e4m3x2_to_f16x2(e[k].x >> 16),
-                         e4m3x2_to_f16x2(e[k].y & 0xFFFFu), e4m3x2_to_f16x2(e[k].y >> 16));
-          *reinterpret_cast<uint4*>(dcol + swz128(row, c16 + 1)) =
-              make_uint4(e4m3x2_to_f16x2(e[k].z & 0xFFFFu), e4m3x2_to_f16x2(e[k].z >> 16),
-                         e4m3x2_to_f16x2(e[k].w & 0xFFFFu), e4m3x2_to_f16x2(e[k].w >> 16));
+          // the codes' two 16-byte halves, the odd one first in the row's second
+          // column block: the two blocks' chunks then fall into different banks
+          const uint32_t a0 = odd ? e[k].z : e[k].x, a1 = odd ? e[k].w : e[k].y;
+          const uint32_t b0 = odd ? e[k].x : e[k].z, b1 = odd ? e[k].y : e[k].w;
+          *reinterpret_cast<uint4*>(dcol + swz128(row, c16 + odd)) =
+              make_uint4(e4m3x2_to_f16x2(a0 & 0xFFFFu), e4m3x2_to_f16x2(a0 >> 16),
+                         e4m3x2_to_f16x2(a1 & 0xFFFFu), e4m3x2_to_f16x2(a1 >> 16));
+          *reinterpret_cast<uint4*>(dcol + swz128(row, c16 + 1 - odd)) =
+              make_uint4(e4m3x2_to_f16x2(b0 & 0xFFFFu), e4m3x2_to_f16x2(b0 >> 16),
+                         e4m3x2_to_f16x2(b1 & 0xFFFFu), e4m3x2_to_f16x2(b1 >> 16));
         }
       }
     } else {
@@ -483,8 +502,8 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
     __syncwarp();
   }
   if (producer) {
-    z_cur = page_row(pg_begin + lane);
-    z_next = page_row(pg_begin + 32 + lane);
+    z_cur = page_row(page_of(lane));
+    z_next = page_row(page_of(32 + lane));
   }
   if constexpr (KV8) {
     if (Cfg::PK > 1 && k_warp) named_barrier(2, Cfg::PK * 32);   // the barriers are set up
@@ -639,10 +658,11 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
           for (int k = 0; k < kTcKeys / 16; ++k) {
             const uint64_t bd = tc::sdesc(vst + k * 2 * 1024, Cfg::KV_BOX, 1024);
             if constexpr (Cfg::PTM) {
-              // 16 keys of P: 8 columns of the group's S buffer, each
-              // 64-key half of P at the start of that half's S columns
-              tc::mma_ts(tO + g * D, tS + (NSB * g + b) * kTcKeys + 64 * (k / 4) + 8 * (k % 4),
-                         bd, ID_O, (j > 0 || k > 0) ? 1u : 0u);
+              // 16 keys of P: 8 columns of the group's S buffer, each 64-key half of
+              // P at the start of that half's S columns (MODE: one half behind the other)
+              const int col = MODE == kTcPlain ? 64 * (k / 4) + 8 * (k % 4) : 8 * k;
+              tc::mma_ts(tO + g * D, tS + (NSB * g + b) * kTcKeys + col, bd, ID_O,
+                         (j > 0 || k > 0) ? 1u : 0u);
             } else {
               const uint64_t a = tc::sdesc(
                   sP + (NSB * g + b) * Cfg::P_BYTES + (k / 4) * Cfg::P_CB + (k % 4) * 32, 16,
@@ -701,7 +721,7 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
     if constexpr (BSC) {
       const int shift = origin / kBS;
       return page_scale_bytes(p.block_tables + (int64_t)n * p.max_blocks,
-                              shift + pg_begin + 32 * q + lane, shift + pg_end, p.ppb_shift,
+                              shift + page_of(32 * q + lane), shift + pg_end, p.ppb_shift,
                               p.num_blocks, p.Hkv, h, ep.k_block_scales, ep.v_block_scales);
     }
     return 0u;
@@ -715,116 +735,40 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
 
   for (int j = 0; j < n_mine; ++j) {
     const int u = NG * j + grp;                         // local tile
-    const int t = t_begin + u;                          // key tile
+    const int t = tile_of(u);                           // key tile
     const int st = u % NST;
     const int b = j % NSB;
     wait(&s_bar[grp][b], (j / NSB) & 1);
     tc::fence_after();
     const uint32_t sbuf = tS + (NSB * grp + b) * kTcKeys + lane_base;
-    // raw scores, 64 keys at a time; keys past this row's causal limit become
-    // -inf (only the halves that cross the limit need the test). A 128-key
-    // tile is read from TMEM twice, for the max and then for P, which keeps
-    // 64 scores in registers
-    constexpr int HALVES = kTcKeys / 64;
-    // (MODE: the code of a half once, for the instruction caches' sake)
-    constexpr int kUnrollHalves = MODE == kTcPlain ? HALVES : 1;
-    // BSC: the score factors and V exponents of the four pages of a 64-key half
-    float kf[4], ev[4];
-    if constexpr (BSC) {
-      if ((u * kTcPages) / 32 != sc_chunk) {
-        sc_cur = sc_next;
-        sc_next = scales_of(++sc_chunk + 1);
-      }
-    }
-    auto load_scales = [&](int hh) {
-      if constexpr (BSC) {
+    if constexpr (MODE == kTcPlain) {
+      // raw scores, 64 keys at a time; keys past this row's causal limit become
+      // -inf (only the halves that cross the limit need the test). A 128-key
+      // tile is read from TMEM twice, for the max and then for P, which keeps
+      // 64 scores in registers
+      constexpr int HALVES = kTcKeys / 64;
+      float x[64];
+      auto load_half = [&](int hh) {
+        uint32_t sv[2][32];
+        tc::ld32(sbuf + hh * 64, sv[0]);
+        tc::ld32(sbuf + hh * 64 + 32, sv[1]);
+        tc::wait_ld();
 #pragma unroll
-        for (int pg = 0; pg < 4; ++pg) {
-          const uint32_t sc =
-              __shfl_sync(0xffffffffu, sc_cur, (u * kTcPages + 4 * hh + pg) % 32);
-          // (not below the least normal number, so that a masked -inf stays -inf)
-          const float f = sl2 * e8m0_value(sc & 0xFFu);
-          kf[pg] = f < 0x1p-126f ? 0x1p-126f : f;
-          ev[pg] = e8m0_log2(sc >> 8);
+        for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(sv[c / 32][c % 32]);
+        const int k0 = t * kTcKeys + hh * 64;
+        if (k0 + 63 > lim) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (k0 + c > lim) x[c] = -INFINITY;
         }
-      }
-    };
-    float x[64];
-    auto load_half = [&](int hh, bool first_time) {
-      uint32_t sv[2][32];
-      tc::ld32(sbuf + hh * 64, sv[0]);
-      tc::ld32(sbuf + hh * 64 + 32, sv[1]);
-      tc::wait_ld();
-#pragma unroll
-      for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(sv[c / 32][c % 32]);
-      const int k0 = t * kTcKeys + hh * 64;
-      if constexpr (MOD) if (first_time) {
-        // the scores themselves, in log2 units
-#pragma unroll
-        for (int c = 0; c < 64; ++c) x[c] *= BSC ? kf[c / kBS] : sl2;
-        if (ep.cap_log2 != 0.f) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) x[c] = softcap_log2(x[c], ep.cap_log2, ep.two_over_cap);
-        }
-        if (ep.slopes != nullptr) {
-          if (k0 + 63 <= pos) {
-            const float b0 = slope * (float)(k0 - pos);
-#pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = fmaf(slope, (float)c, x[c] + b0);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = fmaf(-slope, fabsf((float)(k0 - pos + c)), x[c]);
-          }
-        }
-      }
-      if ((!MOD || first_time) && k0 + 63 > last) {
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (k0 + c > last) x[c] = -INFINITY;
-      }
-      if (MOD && first_time && k0 < lo) {
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (k0 + c < lo) x[c] = -INFINITY;
-      }
-      // MOD: back where they came from, unless they stay in registers until P
-      if (MOD && first_time && hh < HALVES - 1) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          uint32_t v[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(x[32 * w + c]);
-          tc::st32(sbuf + hh * 64 + 32 * w, v);
-        }
-        tc::wait_st();
-      }
-    };
-    float mx, mxw = -INFINITY;                          // largest score; BSC: largest score + ev
-    if constexpr (BSC) {
-      mx = -INFINITY;
-#pragma unroll 1
-      for (int hh = 0; hh < HALVES; ++hh) {
-        load_scales(hh);
-        load_half(hh, true);
-        float pm[4][2];                                 // two chains per page
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          pm[c / kBS][c % 2] = c % kBS < 2 ? x[c] : fmaxf(pm[c / kBS][c % 2], x[c]);
-#pragma unroll
-        for (int pg = 0; pg < 4; ++pg) {
-          const float top = fmaxf(pm[pg][0], pm[pg][1]) * (MOD ? 1.f : kf[pg]);
-          mx = fmaxf(mx, top);
-          mxw = fmaxf(mxw, top + ev[pg]);
-        }
-      }
-    } else {
+      };
       // row max over 8 independent chains, then a tree
       float m8[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) m8[k] = -INFINITY;
-#pragma unroll kUnrollHalves
+#pragma unroll
       for (int hh = 0; hh < HALVES; ++hh) {
-        load_half(hh, true);
+        load_half(hh);
 #pragma unroll
         for (int c = 0; c < 64; ++c) m8[c % 8] = fmaxf(m8[c % 8], x[c]);
       }
@@ -832,106 +776,218 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
       for (int w = 4; w > 0; w >>= 1)
 #pragma unroll
         for (int k = 0; k < w; ++k) m8[k] = fmaxf(m8[k], m8[k + w]);
-      mx = MOD ? m8[0] : m8[0] * sl2;                   // the scale is positive: max commutes
-    }
-    // move a reference only when the row max outgrows it by 2^8
-    float& o_ref = BSC ? w_ref : m_ref;                 // what O is relative to
-    const float o_top = BSC ? mxw : mx;
-    const bool move = o_top > o_ref + kRescaleLog2;
-    const float alpha = move ? (o_ref == -INFINITY ? 0.f : ex2_approx(o_ref - o_top)) : 1.f;
-    if (move) o_ref = o_top;
-    float l_alpha = alpha;
-    if constexpr (BSC) {
-      const bool moves = mx > m_ref + kRescaleLog2;
-      l_alpha = moves ? (m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mx)) : 1.f;
-      if (moves) m_ref = mx;
-    }
-    if (j > 0 && __any_sync(0xffffffffu, move)) {
-      // O must hold every earlier tile of this group before it is scaled
-      wait(&o_bar[grp][(j - 1) % NSB], ((j - 1) / NSB) & 1);
-      tc::fence_after();
+      const float mx = m8[0] * sl2;                       // the scale is positive: max commutes
+      // move the reference max only when the row max outgrows it by 2^8
+      const bool move = mx > m_ref + kRescaleLog2;
+      const float alpha = move ? (m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mx)) : 1.f;
+      if (move) m_ref = mx;
+      if (j > 0 && __any_sync(0xffffffffu, move)) {
+        // O must hold every earlier tile of this group before it is scaled
+        wait(&o_bar[grp][(j - 1) % NSB], ((j - 1) / NSB) & 1);
+        tc::fence_after();
 #pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t ov[32];
-        tc::ld32(tOg + lane_base + c0, ov);
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t ov[32];
+          tc::ld32(tOg + lane_base + c0, ov);
+          tc::wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
+          tc::st32(tOg + lane_base + c0, ov);
+        }
+        tc::wait_st();
+      }
+      // P buffer b was read by the P.V of this group's tile j - NSB
+      if (j >= NSB) wait(&o_bar[grp][b], ((j - NSB) / NSB) & 1);
+      const float ms = m_ref == -INFINITY ? 0.f : m_ref;
+      uint8_t* pPb = pP + (NSB * grp + b) * Cfg::P_BYTES;
+      float rs8[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) rs8[k] = 0.f;
+#pragma unroll
+      for (int it = 0; it < HALVES; ++it) {
+        // PTM: the last half first, from the registers the max pass left it in,
+        // then the others reloaded; P of keys 64 hh .. 64 hh + 63 goes to
+        // columns 64 hh .. 64 hh + 31, the first half of that half's own scores
+        // (already in x), so no score is overwritten before it is read
+        const int hh = Cfg::PTM ? HALVES - 1 - it : it;
+        if (HALVES > 1 && (!Cfg::PTM || it > 0)) load_half(hh);   // (else x holds it)
+        uint32_t pv[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float e[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            e[k] = ex2_approx(fmaf(x[8 * c + k], sl2, -ms));
+            rs8[k] += e[k];
+          }
+          const uint4 w = make_uint4(pack16x2<BF16>(e[0], e[1]), pack16x2<BF16>(e[2], e[3]),
+                                     pack16x2<BF16>(e[4], e[5]), pack16x2<BF16>(e[6], e[7]));
+          if constexpr (Cfg::PTM) {
+            pv[4 * c] = w.x;
+            pv[4 * c + 1] = w.y;
+            pv[4 * c + 2] = w.z;
+            pv[4 * c + 3] = w.w;
+          } else {
+            *reinterpret_cast<uint4*>(pPb + hh * Cfg::P_CB + swz128(r, c)) = w;
+          }
+        }
+        if constexpr (Cfg::PTM) tc::st32(sbuf + hh * 64, pv);
+      }
+      if constexpr (Cfg::PTM) tc::wait_st();
+#pragma unroll
+      for (int w = 4; w > 0; w >>= 1)
+#pragma unroll
+        for (int k = 0; k < w; ++k) rs8[k] += rs8[k + w];
+      l = l * alpha + rs8[0];
+    } else {
+      // A row's scores, CH keys at a time, twice: rewritten (MOD) or as they are for
+      // the maxima, then for P. The loops are not unrolled: a row's worth of
+      // straight-line code beside the producers' does not stay in the instruction
+      // caches (CH = 32 292 us on the long chunk; two chunks unrolled, the second
+      // on its way from tensor memory meanwhile, 326; CH = 16 319).
+      constexpr int CH = 32, NCH = kTcKeys / CH, PPC = CH / kBS;
+      float x[CH], kf[PPC], ev[PPC];
+      if constexpr (BSC) {
+        if ((u * kTcPages) / 32 != sc_chunk) {
+          sc_cur = sc_next;
+          sc_next = scales_of(++sc_chunk + 1);
+        }
+      }
+      auto load = [&](int i) {
+        uint32_t v[CH];
+        tc::ld32(sbuf + i * CH, v);
+        if constexpr (BSC) {
+#pragma unroll
+          for (int pg = 0; pg < PPC; ++pg) {
+            const uint32_t sc =
+                __shfl_sync(0xffffffffu, sc_cur, (u * kTcPages + PPC * i + pg) % 32);
+            // (not below the least normal number, so that a masked -inf stays -inf)
+            const float f = sl2 * e8m0_value(sc & 0xFFu);
+            kf[pg] = f < 0x1p-126f ? 0x1p-126f : f;
+            ev[pg] = e8m0_log2(sc >> 8);
+          }
+        }
         tc::wait_ld();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
-        tc::st32(tOg + lane_base + c0, ov);
+        for (int c = 0; c < CH; ++c) x[c] = __uint_as_float(v[c]);
+      };
+      // keys the row does not see become -inf (only chunks that cross a limit)
+      auto mask = [&](int k0) {
+        if (k0 + CH - 1 > last || (MOD && k0 < lo)) {
+          const unsigned span = (unsigned)(last - lo);
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            if ((unsigned)(k0 - lo + c) > span) x[c] = -INFINITY;
+        }
+      };
+      float mx = -INFINITY, mxw = -INFINITY;              // largest score, largest score + ev
+#pragma unroll 1
+      for (int i = 0; i < NCH; ++i) {
+        load(i);
+        const int k0 = t * kTcKeys + i * CH;
+        if constexpr (MOD) {
+          // the scores themselves, in log2 units
+#pragma unroll
+          for (int c = 0; c < CH; ++c) x[c] *= BSC ? kf[c / kBS] : sl2;
+          if (ep.cap_log2 != 0.f) softcap_log2_row(x, ep.cap_log2, ep.two_over_cap);
+          if (ep.slopes != nullptr) {
+            const float d0 = (float)(k0 - pos);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              const float d = d0 + (float)c;
+              x[c] = fmaf(slope, fminf(d, -d), x[c]);
+            }
+          }
+        }
+        mask(k0);
+        float pm[PPC][4];                                 // four chains per page
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          pm[c / kBS][c % 4] = c % kBS < 4 ? x[c] : fmaxf(pm[c / kBS][c % 4], x[c]);
+#pragma unroll
+        for (int pg = 0; pg < PPC; ++pg) {
+          float top = fmaxf(fmaxf(pm[pg][0], pm[pg][1]), fmaxf(pm[pg][2], pm[pg][3]));
+          if constexpr (!MOD) top *= kf[pg];              // (a positive factor: max commutes)
+          mx = fmaxf(mx, top);
+          if constexpr (BSC) mxw = fmaxf(mxw, top + ev[pg]);
+        }
+        if constexpr (MOD) {
+          uint32_t v[CH];
+#pragma unroll
+          for (int c = 0; c < CH; ++c) v[c] = __float_as_uint(x[c]);
+          tc::st32(sbuf + i * CH, v);
+        }
+      }
+      if constexpr (MOD) tc::wait_st();
+      // move a reference only when the row max outgrows it by 2^8. Where there was
+      // none yet, every P of the row so far was 0, and so is its O: nothing to scale
+      float& o_ref = BSC ? w_ref : m_ref;                 // what O is relative to
+      const float o_top = BSC ? mxw : mx;
+      const bool move = o_top > o_ref + kRescaleLog2;
+      const bool scales_o = move && o_ref != -INFINITY;
+      const float alpha = scales_o ? ex2_approx(o_ref - o_top) : 1.f;
+      float l_alpha = alpha;
+      if constexpr (BSC) {
+        const bool moves = mx > m_ref + kRescaleLog2;
+        l_alpha = moves && m_ref != -INFINITY ? ex2_approx(m_ref - mx) : 1.f;
+        if (moves) m_ref = mx;
+      }
+      if (move) o_ref = o_top;
+      if (j > 0 && __any_sync(0xffffffffu, scales_o)) {
+        // O must hold every earlier tile of this group before it is scaled
+        wait(&o_bar[grp][(j - 1) % NSB], ((j - 1) / NSB) & 1);
+        tc::fence_after();
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t ov[32];
+          tc::ld32(tOg + lane_base + c0, ov);
+          tc::wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
+          tc::st32(tOg + lane_base + c0, ov);
+        }
+        tc::wait_st();
+      }
+      // P, packed over the scores already read: keys 32 i .. of the tile go to
+      // columns 16 i .. of the buffer. BSC: P of page pg is its probabilities times
+      // 2^-back, back = w_ref - ev - m_ref: relative to O's reference, with the page's
+      // V scale in it. A page whose V scale is so small that its P would leave fp32
+      // (back above 80: its part of O is nothing) keeps a P of 2^-80 times the
+      // probabilities, 0 in f16, so that its sum stays exact.
+      const float ms = m_ref == -INFINITY ? 0.f : m_ref;
+      const float wr = w_ref == -INFINITY ? 0.f : w_ref;
+      float sum = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < NCH; ++i) {
+        load(i);
+        if constexpr (!MOD) mask(t * kTcKeys + i * CH);
+        uint32_t pv[CH / 2];
+#pragma unroll
+        for (int pg = 0; pg < PPC; ++pg) {
+          float back = 0.f;
+          if constexpr (BSC) {
+            const float d = wr - ev[pg] - ms;
+            back = d > 80.f ? 80.f : d;
+          }
+          const float sub = ms + back;
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < kBS; c += 2) {
+            const int k = kBS * pg + c;
+            const float e0 = ex2_approx(MOD ? x[k] - sub : fmaf(x[k], kf[pg], -sub));
+            const float e1 = ex2_approx(MOD ? x[k + 1] - sub : fmaf(x[k + 1], kf[pg], -sub));
+            s4[c % 4] += e0;
+            s4[c % 4 + 1] += e1;
+            pv[k / 2] = pack16x2<BF16>(e0, e1);
+          }
+          const float ps = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          sum = BSC ? fmaf(ps, ex2_approx(back), sum) : sum + ps;
+        }
+        tc::st16(sbuf + i * (CH / 2), pv);
       }
       tc::wait_st();
+      l = l * l_alpha + sum;
     }
-    // P buffer b was read by the P.V of this group's tile j - NSB
-    if (j >= NSB) wait(&o_bar[grp][b], ((j - NSB) / NSB) & 1);
-    const float ms = m_ref == -INFINITY ? 0.f : m_ref;
-    uint8_t* pPb = pP + (NSB * grp + b) * Cfg::P_BYTES;
-    float rs8[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) rs8[k] = 0.f;
-#pragma unroll kUnrollHalves
-    for (int it = 0; it < HALVES; ++it) {
-      // PTM: the last half first, from the registers the max pass left it in,
-      // then the others reloaded; P of keys 64 hh .. 64 hh + 63 goes to
-      // columns 64 hh .. 64 hh + 31, the first half of that half's own scores
-      // (already in x), so no score is overwritten before it is read
-      const int hh = Cfg::PTM ? HALVES - 1 - it : it;
-      if (HALVES > 1 && (!Cfg::PTM || it > 0)) {
-        load_scales(hh);
-        load_half(hh, false);
-      }                                                 // (else x, kf and ev hold it)
-      uint32_t pv[32];
-      // BSC: P of page pg is its probabilities times 2^-back, back = w_ref - ev -
-      // m_ref: relative to O's reference, with the page's V scale in it. A page
-      // whose V scale is so small that its P would leave fp32 (back above 80: its
-      // part of O is nothing) keeps a P of 2^-80 times the probabilities, 0 in
-      // f16, so that its sum stays exact.
-      float ps[4], back[4];
-      if constexpr (BSC) {
-        const float wr = w_ref == -INFINITY ? 0.f : w_ref;
-#pragma unroll
-        for (int pg = 0; pg < 4; ++pg) {
-          const float d = wr - ev[pg] - ms;
-          back[pg] = d > 80.f ? 80.f : d;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        float e[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if constexpr (BSC)                             // one page: 8 c / 16
-            e[k] = MOD ? ex2_approx(x[8 * c + k] - (ms + back[c / 2]))
-                       : ex2_approx(fmaf(x[8 * c + k], kf[c / 2], -(ms + back[c / 2])));
-          else
-            e[k] = MOD ? ex2_approx(x[8 * c + k] - ms) : ex2_approx(fmaf(x[8 * c + k], sl2, -ms));
-          if constexpr (!BSC) rs8[k] += e[k];
-        }
-        // BSC: page c / 2 of the half's sum of P
-        if constexpr (BSC)
-          ps[c / 2] = (c % 2 ? ps[c / 2] : 0.f) + ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-        const uint4 w = make_uint4(pack16x2<BF16>(e[0], e[1]), pack16x2<BF16>(e[2], e[3]),
-                                   pack16x2<BF16>(e[4], e[5]), pack16x2<BF16>(e[6], e[7]));
-        if constexpr (Cfg::PTM) {
-          pv[4 * c] = w.x;
-          pv[4 * c + 1] = w.y;
-          pv[4 * c + 2] = w.z;
-          pv[4 * c + 3] = w.w;
-        } else {
-          *reinterpret_cast<uint4*>(pPb + hh * Cfg::P_CB + swz128(r, c)) = w;
-        }
-      }
-      if constexpr (Cfg::PTM) tc::st32(sbuf + hh * 64, pv);
-      if constexpr (BSC) {
-#pragma unroll
-        for (int pg = 0; pg < 4; ++pg) rs8[pg] = fmaf(ps[pg], ex2_approx(back[pg]), rs8[pg]);
-      }
-    }
-    if constexpr (Cfg::PTM) tc::wait_st();
-#pragma unroll
-    for (int w = 4; w > 0; w >>= 1)
-#pragma unroll
-      for (int k = 0; k < w; ++k) rs8[k] += rs8[k + w];
-    l = l * l_alpha + rs8[0];
     // V rows with no data for this tile (past the context, or pages not
     // loaded) meet weight 0 in P: zero them so their contents cannot make NaN.
     // The group's threads share the rows; the P.V waits for all of them.
@@ -1170,9 +1226,9 @@ static int prefill_tc_sms(int dev) {
   return n;
 }
 
-// The _ext calls: one CTA per query tile when that fills at
-// least half of the GPU; otherwise a cluster of two per tile, each taking half
-// of the key tiles.
+// The _ext calls: one CTA per query tile when that fills at least half of the
+// GPU; otherwise a cluster of two per tile, each taking
+// half of the key tiles.
 template <int D, int KV, bool QBF16, int MODE>
 static pkv_status launch_tc_ext(const PrefillExtParams& ep, const CUtensorMap& tmQ,
                                 const CUtensorMap& tmK, const CUtensorMap& tmV,
