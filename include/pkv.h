@@ -415,7 +415,10 @@ pkv_status rope_reshape_and_cache(void* query, const void* key, const void* valu
  *   cos_sin_cache: as in rope_reshape_and_cache, fp32 [max_position, rot_dim],
  *           the row of a token being its position; or NULL for no rotation
  *           (max_position, rot_dim, neox_style and the queries are then
- *           ignored). Keys are rotated and rounded to src_dtype first.
+ *           ignored). A rotated element is the fp32 value nearest to the exact
+ *           y1 or y2, rounded to src_dtype; keys are rotated first. (Not through
+ *           double as in rope_reshape_and_cache: about one element in 2^17, next
+ *           to a midpoint of src_dtype, may differ by a step between the calls.)
  *   query, query_out: [total_q_tokens, Hq, D] src_dtype, the rotated queries;
  *           query_out may be query itself (in place), or both NULL.
  *   A block that the call writes belongs to one sequence: copy a shared,

@@ -9,15 +9,13 @@
 //   exponent s if s >= e, else takes e and its other slots are re-encoded:
 //   code <- E4M3(code * 2^(s - e)). New codes are E4M3(x * 2^-e').
 //
-// Rotation: y1 = x1 c - x2 s, y2 = x2 c + x1 s, rounded once to the source type.
-// fp32 alone is not enough for that (its own rounding may move a sum across a
-// midpoint of the 16-bit type, about one element in 2^12 of f16), and doubles are
-// slow, so the sums are carried as unevaluated pairs: the products with their
-// errors (fma), their sum with its error (Knuth's two-sum), the parts added up.
-// The pair is then rounded to odd in fp32 - truncated, its last bit set if
-// anything was cut off - which leaves the second rounding, to 16 bits, the same as
-// one of the exact sum. y1 and y2 of a pair run through the packed two-float
-// instructions side by side.
+// Rotation: y1 = x1 c - x2 s, y2 = x2 c + x1 s, each the fp32 value nearest to the
+// exact sum, then rounded to the source type. (The plain fp32 sum is off by up to
+// its products' rounding, which cancellation makes large against the sum; one element
+// in 2^12 of f16 would land on the other side of a midpoint.) Doubles are slow, so the
+// sum is carried as an unevaluated pair: the products with their errors (fma), their
+// sum with its error (Knuth's two-sum), the parts added up. y1 and y2 of a pair run
+// through the packed two-float instructions side by side.
 //
 // Work decomposition. Tokens of a sequence that fall into one block are
 // consecutive rows (a run of at most BS), so a run, not a token, is the unit:
@@ -135,14 +133,6 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float f) {
   return out;
 }
 
-// r + rem (|rem| at most half a unit in r's last place) rounded to odd.
-__device__ __forceinline__ float round_odd(float r, float rem) {
-  const uint32_t b = __float_as_uint(r);
-  const bool cut = fabsf(rem) > 0.f;
-  const bool over = cut && (int32_t)(b ^ __float_as_uint(rem)) < 0;   // r lies past the sum
-  return __uint_as_float((b - (over ? 1u : 0u)) | (cut ? 1u : 0u));
-}
-
 // The angles of one item: 8 cosines and 8 sines.
 struct Angles {
   float4 c[2], s[2];
@@ -180,11 +170,10 @@ __device__ __forceinline__ Pair8 rotate_pairs(const Pair8& in, const Angles& an)
     const f2 err = sub2(sub2(p, bb), add2(nq, sub2(sum, bb)));       // what the sum leaves
     const f2 rest = add2(err, add2(qe, pe));
     const f2 r = add2(sum, rest);
-    const f2 rem = sub2(rest, sub2(r, sum));
     finite = fma2(r, pack_f2(0.f, 0.f), finite);
-    const float2 rr = unpack_f2(r), mm = unpack_f2(rem);
-    y1[e] = round_odd(rr.x, mm.x);
-    y2[e] = round_odd(rr.y, mm.y);
+    const float2 y = unpack_f2(r);
+    y1[e] = y.x;
+    y2[e] = y.y;
   }
   const float2 f = unpack_f2(finite);
   if (!(f.x == 0.f && f.y == 0.f)) {

@@ -26,13 +26,9 @@ def exponent(amax):
 
 
 def round16(x, dtype):
-    """Doubles to the nearest value of a 16-bit type, in one rounding. (torch converts a double
-    by way of fp32: a sum that fp32 rounds onto a midpoint of the 16-bit type is then rounded a
-    second time, about one element in 2^17.)"""
-    bits, low = (8, -125) if dtype == torch.bfloat16 else (11, -13)
-    _, e = torch.frexp(x)
-    step = torch.exp2(torch.clamp(e, min=low).double() - bits)
-    return (torch.round(x / step) * step).to(dtype)
+    """Doubles to the nearest fp32 value, then to the nearest value of a 16-bit type: the
+    rounding the append defines for rotated elements."""
+    return x.float().to(dtype)
 
 
 def rotate(x, pos, cos_sin, neox):
