@@ -1,5 +1,5 @@
 """One attention-layer pass of a continuous-batching step, composed from the
-three C-ABI calls (argument marshalling and stream plumbing only).
+C-ABI calls (argument marshalling and stream plumbing only).
 
 A decode step writes the new token of every sequence into its slot
 (reshape_and_cache) and then runs decode attention over the paged cache
@@ -206,3 +206,60 @@ class MixedStep:
         if self.mode == "varlen":
             return [self.out_all]
         return [self.decode.out, self.prefill_out]
+
+
+class BlockScaledStep:
+    """One attention-layer pass of a continuous-batching step over a cache held in E4M3 with
+    a scale per block and KV head: the append of every new token (queries and keys rotated
+    with cos_sin, if given), then decode attention of the first num_decode sequences (one new
+    token each) and prefill attention of the others' chunks, with the scores capped, biased
+    or limited to a window where the options say so.
+
+    q, new_k, new_v: [tokens, heads, D] of all sequences in order, cu_q_lens [n + 1] their
+    offsets, seq_lens including the new tokens. run() works on the buffers given here, so it
+    can be captured into a CUDA graph and replayed with new contents: max_seq_len bounds the
+    decode sequences' contexts and max_q_len the chunks, at every replay."""
+
+    def __init__(self, k_cache, v_cache, k_scales, v_scales, q, new_k, new_v, block_tables,
+                 seq_lens, cu_q_lens, num_decode, scale, max_seq_len, max_q_len=0, cos_sin=None,
+                 neox_style=True, softcap=0.0, window=0, alibi_slopes=None):
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self.k_scales, self.v_scales = k_scales, v_scales
+        self.q, self.new_k, self.new_v = q, new_k, new_v
+        self.block_tables, self.seq_lens, self.cu_q_lens = block_tables, seq_lens, cu_q_lens
+        self.num_decode, self.scale = int(num_decode), float(scale)
+        self.max_seq_len, self.max_q_len = int(max_seq_len), int(max_q_len)
+        self.cos_sin, self.neox_style = cos_sin, neox_style
+        self.opts = dict(softcap=softcap, window=window, alibi_slopes=alibi_slopes)
+        # the queries as attention takes them: rotated, or as they come
+        self.q_rot = torch.empty_like(q) if cos_sin is not None else q
+        self.out = torch.empty_like(q)
+        _, Hq, D = q.shape
+        ws = B.paged_attn_decode_ext_workspace_size(self.num_decode, Hq, k_cache.shape[1], D,
+                                                    self.max_seq_len, window)
+        self.workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=q.device)
+
+    def append(self, stream=None):
+        rot = self.cos_sin is not None
+        B.rope_append_block_scaled(self.new_k, self.new_v, self.k_cache, self.v_cache,
+                                   self.k_scales, self.v_scales, self.block_tables, self.seq_lens,
+                                   self.cu_q_lens, query=self.q if rot else None,
+                                   query_out=self.q_rot if rot else None,
+                                   cos_sin_cache=self.cos_sin, neox_style=self.neox_style,
+                                   stream=stream)
+
+    def run(self, stream=None):
+        self.append(stream)
+        nd = self.num_decode
+        if nd < self.seq_lens.shape[0]:
+            # the chunks' rows: their offsets in cu_q_lens are rows of q_rot and out
+            B.paged_attn_prefill_chunk_ext(self.out, self.q_rot, self.k_cache, self.v_cache,
+                                           self.block_tables[nd:], self.seq_lens[nd:],
+                                           self.cu_q_lens[nd:], self.scale, self.max_q_len,
+                                           self.k_scales, self.v_scales, stream=stream,
+                                           **self.opts)
+        if nd > 0:
+            B.paged_attn_decode_ext(self.out[:nd], self.q_rot[:nd], self.k_cache, self.v_cache,
+                                    self.block_tables[:nd], self.seq_lens[:nd], self.scale,
+                                    self.max_seq_len, self.k_scales, self.v_scales,
+                                    workspace=self.workspace, stream=stream, **self.opts)
