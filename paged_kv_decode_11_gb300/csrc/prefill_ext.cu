@@ -260,7 +260,11 @@ __global__ void __launch_bounds__((kConsumers + 1) * 32)
           const int e = w >> 1;
           const float pr = exp2f(s[j][w] - ms[e]);
           l[e] += pr;
-          s[j][w] = BSC ? exp2f(s[j][w] + (evl[j / 2] - mv[e])) : pr;
+          // (a masked score has weight 0 even on a page whose scale is NaN)
+          if constexpr (BSC)
+            s[j][w] = s[j][w] == -INFINITY ? 0.f : exp2f(s[j][w] + (evl[j / 2] - mv[e]));
+          else
+            s[j][w] = pr;
         }
 #pragma unroll
       for (int tt = 0; tt < D / 8; ++tt)

@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   float slope = 0.f;
   if constexpr (MOD) {
     last = max(pos, prefix - origin - 1);
-    if (ep.window > 0) lo = pos - ep.window + 1;
+    if (ep.window > 0) lo = max(0, pos - ep.window + 1);
     if (ep.slopes != nullptr) slope = ep.slopes[hq] * kLog2e;
   }
   // BSC: a lane's share of the scale bytes (K low, V high) of the next 32 pages
@@ -847,6 +847,8 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
       // on its way from tensor memory meanwhile, 326; CH = 16 319).
       constexpr int CH = 32, NCH = kTcKeys / CH, PPC = CH / kBS;
       float x[CH], kf[PPC], ev[PPC];
+      float nan_or_0[PPC];                                // BSC: NaN where a scale of the page is
+      bool nan_scale = false;
       if constexpr (BSC) {
         if ((u * kTcPages) / 32 != sc_chunk) {
           sc_cur = sc_next;
@@ -861,23 +863,29 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
           for (int pg = 0; pg < PPC; ++pg) {
             const uint32_t sc =
                 __shfl_sync(0xffffffffu, sc_cur, (u * kTcPages + PPC * i + pg) % 32);
+            const bool bad = (sc & 0xFFu) == 255u || sc >> 8 == 255u;
+            nan_scale = (pg > 0 && nan_scale) || bad;
+            nan_or_0[pg] = bad ? __int_as_float(0x7FFFFFFF) : 0.f;
             // (not below the least normal number, so that a masked -inf stays -inf)
-            const float f = sl2 * e8m0_value(sc & 0xFFu);
-            kf[pg] = f < 0x1p-126f ? 0x1p-126f : f;
-            ev[pg] = e8m0_log2(sc >> 8);
+            kf[pg] = fmaxf(sl2 * pow2_any(min((int)(sc & 0xFFu), 254) - kE8M0Bias), 0x1p-126f);
+            ev[pg] = (float)((int)(sc >> 8) - kE8M0Bias);
           }
         }
         tc::wait_ld();
 #pragma unroll
         for (int c = 0; c < CH; ++c) x[c] = __uint_as_float(v[c]);
       };
-      // keys the row does not see become -inf (only chunks that cross a limit)
+      // Keys the row does not see become -inf (only in chunks that cross a limit).
+      // BSC: keys of a page whose scale is NaN become NaN for the rows that see them
+      // (and only for those: a masked score times a NaN factor would be one too).
       auto mask = [&](int k0) {
-        if (k0 + CH - 1 > last || (MOD && k0 < lo)) {
+        if (k0 + CH - 1 > last || (MOD && k0 < lo) || (BSC && nan_scale)) {
           const unsigned span = (unsigned)(last - lo);
 #pragma unroll
-          for (int c = 0; c < CH; ++c)
+          for (int c = 0; c < CH; ++c) {
+            if constexpr (BSC) x[c] += nan_or_0[c / kBS];
             if ((unsigned)(k0 - lo + c) > span) x[c] = -INFINITY;
+          }
         }
       };
       float mx = -INFINITY, mxw = -INFINITY;              // largest score, largest score + ev

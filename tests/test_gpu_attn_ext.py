@@ -317,6 +317,36 @@ def test_prefill_block_scales_far_apart():
     assert (err <= tol).all()
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=9.0), dict(d=64), dict(d=256), dict(bs=64)])
+@pytest.mark.parametrize("which", ["ks", "vs"])
+def test_prefill_nan_scale_reaches_the_rows_that_see_it(which, kw):
+    c = Case(19, [(20, 180), (30, 20)], **kw)
+    ref = c.want()
+    bs = c.k.shape[2]
+    block = 100 // bs
+    getattr(c, which)[c.tables[0, block].long(), 1] = 255
+    out, _ = c.prefill()
+    ok()
+    first = max(0, block * bs - 20)                    # the first row that sees the block
+    assert out[first:180, 4:].isnan().all()
+    c.check((out, None), ref, list(range(first)) + list(range(180, 200)))
+    tol = R.tolerance(ref, c.q.dtype, c.p_dtype, c.softcap)
+    assert ((out.double() - ref.out).abs() <= tol)[:, :4].all()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(kv="same", spread=1, alibi=True), dict(d=256)])
+def test_largest_window_sees_everything(kw):
+    c = Case(20, [(200, 70), (0, 33), (5, 1)], **kw)
+    for w in (2 ** 31 - 1, 271):
+        c.prefix = None
+        got = c.prefill(window=w)
+        c.check(got)
+        c.prefix = torch.tensor([260, 33, -1], dtype=torch.int32).cuda()
+        got = c.prefill(window=w)
+        c.check(got)
+    ok()
+
+
 def test_prefill_bad_sequences():
     c = Case(13, [(50, 10), (3, 20), (70, 8)])
     ref = c.want()
