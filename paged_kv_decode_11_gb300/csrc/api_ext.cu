@@ -222,8 +222,9 @@ pkv_status paged_attn_prefill_chunk_ext(void* out, const void* q, pkv_dtype q_dt
   ep.cap_log2 = softcap * kLog2eHost;
   ep.two_over_cap = softcap > 0.f ? 2.f / softcap : 0.f;
   ep.window = window;
-  return launch_prefill_ext(ep, head_dim, q_dtype, page_dtype, block_scaled, tmQ, tmK, tmV,
-                            reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return block_scaled ? launch_prefill_block(ep, head_dim, q_dtype, tmQ, tmK, tmV, s)
+                      : launch_prefill_mod(ep, head_dim, q_dtype, kv_dtype, tmQ, tmK, tmV, s);
 }
 
 pkv_status rope_append_block_scaled(const void* key, const void* value, pkv_dtype src_dtype,

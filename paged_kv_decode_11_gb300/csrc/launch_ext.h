@@ -67,17 +67,15 @@ struct PrefillExtParams {
   int window;                       // keys a row sees, counting its own; 0 = all
 };
 
-// Takes the tensor-core kernel where there is one (prefill_tc_supported), else
-// the m16n8k16 one (E4M3 at head_dim 256). tmQ as for launch_prefill_tc.
-pkv_status launch_prefill_ext(const PrefillExtParams& p, int head_dim, pkv_dtype q_dtype,
-                              pkv_dtype kv_dtype, bool block_scaled, const CUtensorMap& tmQ,
-                              const CUtensorMap& tmK, const CUtensorMap& tmV, cudaStream_t stream);
-pkv_status launch_prefill_tc_block(const PrefillExtParams& p, int head_dim, pkv_dtype q_dtype,
-                                   const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                                   const CUtensorMap& tmV, cudaStream_t stream);
-pkv_status launch_prefill_tc_mod(const PrefillExtParams& p, int head_dim, pkv_dtype q_dtype,
-                                 pkv_dtype kv_dtype, const CUtensorMap& tmQ,
-                                 const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                 cudaStream_t stream);
+// Over block scales (E4M3, head_dim 64, 128 or 256), with modified scores or not.
+// tmQ as for launch_prefill_tc.
+pkv_status launch_prefill_block(const PrefillExtParams& p, int head_dim, pkv_dtype q_dtype,
+                                const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                const CUtensorMap& tmV, cudaStream_t stream);
+// Over the other caches, with modified scores (or none).
+pkv_status launch_prefill_mod(const PrefillExtParams& p, int head_dim, pkv_dtype q_dtype,
+                              pkv_dtype kv_dtype, const CUtensorMap& tmQ,
+                              const CUtensorMap& tmK, const CUtensorMap& tmV,
+                              cudaStream_t stream);
 
 }  // namespace pkv

@@ -1,4 +1,4 @@
-// prefill_tc_ext.cu — the tensor-core chunked prefill (prefill_tc_kernel.cuh) over
+// prefill_block.cu — the tensor-core chunked prefill (prefill_tc_kernel.cuh) over
 // E4M3 blocks with a scale per block and KV head, with and without modified
 // scores.
 #include "prefill_tc_kernel.cuh"
@@ -13,12 +13,15 @@ static pkv_status launch_q(const PrefillExtParams& p, pkv_dtype q_dtype, const C
              : launch_tc_ext<D, KV_E4M3, false, MODE>(p, tmQ, tmK, tmV, stream);
 }
 
-pkv_status launch_prefill_tc_block(const PrefillExtParams& p, int head_dim, pkv_dtype q_dtype,
-                                   const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                                   const CUtensorMap& tmV, cudaStream_t stream) {
+pkv_status launch_prefill_block(const PrefillExtParams& p, int head_dim, pkv_dtype q_dtype,
+                                const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                const CUtensorMap& tmV, cudaStream_t stream) {
   const bool mod = p.cap_log2 != 0.f || p.slopes != nullptr || p.window > 0 ||
                    p.prefix_lens != nullptr;
   constexpr int kBoth = kTcBlockScales | kTcModScores;
+  if (head_dim == 256)
+    return mod ? launch_q<256, kBoth>(p, q_dtype, tmQ, tmK, tmV, stream)
+               : launch_q<256, kTcBlockScales>(p, q_dtype, tmQ, tmK, tmV, stream);
   if (head_dim == 128)
     return mod ? launch_q<128, kBoth>(p, q_dtype, tmQ, tmK, tmV, stream)
                : launch_q<128, kTcBlockScales>(p, q_dtype, tmQ, tmK, tmV, stream);

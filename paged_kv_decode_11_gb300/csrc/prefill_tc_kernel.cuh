@@ -1,8 +1,8 @@
 // prefill_tc_kernel.cuh — causal chunked-prefill attention on the
 // fifth-generation tensor cores (tcgen05): 16-bit caches at head_dim 64, 128
 // and 256, E4M3 caches at 64 and 128. Instantiated by prefill_tc.cu, and with
-// block scales and modified scores (MODE) by prefill_tc_ext.cu and
-// prefill_tc_mod.cu.
+// block scales and modified scores (MODE) by prefill_block.cu and
+// prefill_mod.cu.
 //
 // Follows "Chunked Prefill" (Litellama, Features: a long prompt enters the
 // batch as chunks of new query tokens attending their cached context) with
@@ -106,8 +106,8 @@ struct PrefillTcCfg {
   // columns (two 16-bit values per 32-bit column) and the P.V MMAs read it
   // there, which frees the shared P buffers for deeper K and V rings
   static constexpr bool PTM = WIDE || MODE != kTcPlain;
-  static constexpr int PK = WIDE ? 4 : 1;
-  static constexpr int PV = WIDE ? 3 : 1;
+  static constexpr int PK = WIDE || SHARE ? 4 : 1;
+  static constexpr int PV = WIDE || SHARE ? 3 : 1;
   static constexpr int WARPS = 4 * NG + PK + 1 + PV;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int W_K = 4 * NG, W_MMA = 4 * NG + PK, W_V = 4 * NG + PK + 1;
@@ -129,7 +129,7 @@ struct PrefillTcCfg {
   static constexpr int RING_BYTES = NST * KV_BYTES;          // one ring (K, then V)
   static constexpr int P_CB = kTcRows * 128;                 // 64 keys of a P buffer
   static constexpr int P_BYTES = (KEYS / 64) * P_CB;         // one P buffer (NSB per group)
-  static constexpr int NSS = KV8 ? (WIDE ? 2 : 4) : 0;       // staging stages per operand
+  static constexpr int NSS = !KV8 ? 0 : !SHARE ? 4 : WIDE ? 2 : 1;   // staging stages per operand
   static constexpr int STG_PAGE = kBS * D;                   // one E4M3 page
   static constexpr int STG_BYTES = PAGES * STG_PAGE;         // one staged E4M3 tile
   static constexpr int SMEM_BYTES =
@@ -376,7 +376,11 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
       uint8_t* dst = stage_x + (u % NSS) * Cfg::STG_BYTES;
       for (int pg = pw; pg < npg; pg += np) {
         const int z = __shfl_sync(0xffffffffu, z_cur, (u * kTcPages + pg) % 32);
-        if (lane == 0) tma_load_3d(dst + pg * Cfg::STG_PAGE, tmap, bar, 0, 0, z);
+        using Geo8 = PageGeom<D, KV_E4M3>;
+        if (lane == 0)
+          for (int bx = 0; bx < Geo8::NBOX; ++bx)          // (two at D = 256)
+            tma_load_3d(dst + pg * Cfg::STG_PAGE + bx * Geo8::BOX_BYTES, tmap, bar,
+                        bx * Geo8::BOX_ELEMS, 0, z);
       }
     } else {
       const int st = u % NST;
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
     const int x = lane % CPR, rsub = lane / CPR;
     uint8_t* dcol = ring_x + st * Cfg::KV_BYTES + (x / 4) * Cfg::KV_BOX;
     const int c16 = 2 * (x % 4);
-    const int odd = x / 4;                               // (column block: 0, 1 at D = 128)
+    const int odd = (x / 4) & 1;                         // of the chunk's 64-element column block
     if constexpr (Cfg::SHARE) {
       // this producer's pages one by one, a page's reads ahead of its stores; a
       // loop, not unrolled further: with a tile's worth of straight-line code here
@@ -428,8 +432,8 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
 #pragma unroll
         for (int k = 0; k < kBS / RPI; ++k) {
           const int row = pg * kBS + k * RPI + rsub;
-          // the codes' two 16-byte halves, the odd one first in the row's second
-          // column block: the two blocks' chunks then fall into different banks
+          // the codes' two 16-byte halves, the odd one first in every second column
+          // block: the chunks that eight lanes store then fall into different banks
           const uint32_t a0 = odd ? e[k].z : e[k].x, a1 = odd ? e[k].w : e[k].y;
           const uint32_t b0 = odd ? e[k].x : e[k].z, b1 = odd ? e[k].y : e[k].w;
           *reinterpret_cast<uint4*>(dcol + swz128(row, c16 + odd)) =
