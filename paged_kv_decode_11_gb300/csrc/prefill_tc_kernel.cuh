@@ -83,7 +83,10 @@ constexpr int kTcPlain = 0, kTcBlockScales = 1, kTcModScores = 2;   // MODE bits
 // Long chunk of block scales (2,048 on 4,096, D = 128): 292 us; with one group over
 // three buffers 302, two groups over 64-key tiles 358. The producers of an E4M3
 // operand split a tile by pages (SHARE), each staging and converting its own; with
-// one converting warp per operand that chunk took 558 us.
+// one converting warp per operand that chunk took 558 us. At D = 256 the P in tensor
+// memory leaves an E4M3 cache's staging room beside the query tile, and the seven
+// producers are worth having with a 16-bit one too (2,048 on 4,096 at Hq 16 / Hkv 8
+// with a bias: 285 us with one per operand, 239 with seven).
 template <int D, int NST, bool KV8 = false, bool ALONE = true, int MODE = kTcPlain>
 struct PrefillTcCfg {
   // 128-key tiles (WIDE): one softmax group over two S buffers in tensor
@@ -106,8 +109,8 @@ struct PrefillTcCfg {
   // columns (two 16-bit values per 32-bit column) and the P.V MMAs read it
   // there, which frees the shared P buffers for deeper K and V rings
   static constexpr bool PTM = WIDE || MODE != kTcPlain;
-  static constexpr int PK = WIDE || SHARE ? 4 : 1;
-  static constexpr int PV = WIDE || SHARE ? 3 : 1;
+  static constexpr int PK = WIDE || MODE != kTcPlain ? 4 : 1;
+  static constexpr int PV = WIDE || MODE != kTcPlain ? 3 : 1;
   static constexpr int WARPS = 4 * NG + PK + 1 + PV;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int W_K = 4 * NG, W_MMA = 4 * NG + PK, W_V = 4 * NG + PK + 1;
