@@ -80,8 +80,8 @@ constexpr int kTcPlain = 0, kTcBlockScales = 1, kTcModScores = 2;   // MODE bits
 // The MODE kernels always run alone, in 128-key tiles up to D = 128, with two
 // softmax groups over one S buffer each: their softmax has more work per key (scales
 // per page, rewritten scores), so one group's runs while the other's products do.
-// Long chunk of block scales (2,048 on 4,096, D = 128): 292 us; with one group over
-// three buffers 302, two groups over 64-key tiles 358. The producers of an E4M3
+// Long chunk of block scales (2,048 on 4,096, 32 / 8 heads, D = 128): 291 us, 591
+// TFLOP/s; with one group over three buffers 302, two groups over 64-key tiles 358. The producers of an E4M3
 // operand split a tile by pages (SHARE), each staging and converting its own; with
 // one converting warp per operand that chunk took 558 us. At D = 256 the P in tensor
 // memory leaves an E4M3 cache's staging room beside the query tile, and the seven
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
       // A row's scores, CH keys at a time, twice: rewritten (MOD) or as they are for
       // the maxima, then for P. The loops are not unrolled: a row's worth of
       // straight-line code beside the producers' does not stay in the instruction
-      // caches (CH = 32 292 us on the long chunk; two chunks unrolled, the second
+      // caches (CH = 32 291 us on the long chunk; two chunks unrolled, the second
       // on its way from tensor memory meanwhile, 326; CH = 16 319).
       constexpr int CH = 32, NCH = kTcKeys / CH, PPC = CH / kBS;
       float x[CH], kf[PPC], ev[PPC];
