@@ -16,6 +16,13 @@ namespace pkv {
 constexpr int kE8M0Bias = 127;
 constexpr int kBlockMinExp = -60;       // smallest exponent the append gives a block
 
+// The _ext attentions put a weight's reference this far (log2) below the largest
+// score: the weights that are rounded to 16 bits start at 2^7 and may grow to 2^15
+// before the reference moves, and f16 holds those down to 2^-21 of the largest in full
+// precision (2^-14 with a reference at the maximum). That shows where the largest
+// weights meet zeros in V.
+constexpr float kWeightHeadLog2 = 7.f;
+
 // 2^e for e in [-127, 127] (2^-127 is subnormal).
 __device__ __forceinline__ float pow2_any(int e) {
   return __int_as_float(e == -127 ? 0x00400000 : (e + 127) << 23);

@@ -242,9 +242,10 @@ __global__ void __launch_bounds__(NW * 32)
       kq_page<D, KV, NT>(s, qf, kpage, lane);
     }
 
-    // online softmax in the log2 domain, against references per column that
-    // move only when the page's max outgrows them by kRefSlackLog2, so the
-    // accumulators are rescaled rarely (weights stay below 2^8)
+    // online softmax in the log2 domain, against references per column that lie
+    // kWeightHeadLog2 below a maximum and move only when the page's outgrows that
+    // by kRefSlackLog2, so the accumulators are rescaled rarely (weights stay below
+    // 2^15)
     const bool v0 = tbase + tk0 < tok1 && tbase + tk0 >= first;
     const bool v8 = tbase + tk8 < tok1 && tbase + tk8 >= first;
     const float back0 = (float)(ctx - 1 - (tbase + tk0)), back8 = (float)(ctx - 1 - (tbase + tk8));
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(NW * 32)
         x8 = fmaf(-slope[nt][e], back8, x8);
         s[nt][e] = v0 ? x0 : -INFINITY;
         s[nt][2 + e] = v8 ? x8 : -INFINITY;
-        pmax[nt][e] = col_max8(fmaxf(s[nt][e], s[nt][2 + e]));
+        pmax[nt][e] = col_max8(fmaxf(s[nt][e], s[nt][2 + e])) - kWeightHeadLog2;
         move |= pmax[nt][e] > m[nt][e] + kRefSlackLog2;
         if constexpr (BSC) move |= pmax[nt][e] + evl > mw[nt][e] + kRefSlackLog2;
       }

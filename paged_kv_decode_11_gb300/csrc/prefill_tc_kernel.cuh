@@ -934,20 +934,22 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
         }
       }
       if constexpr (MOD) tc::wait_st();
-      // move a reference only when the row max outgrows it by 2^8. Where there was
-      // none yet, every P of the row so far was 0, and so is its O: nothing to scale
+      // Move P's reference only when P would pass 2^15, and then to 2^7 below the row's
+      // maximum (kWeightHeadLog2). Where there was none yet, every P of the row so
+      // far was 0, and so is its O: nothing to scale
       float& o_ref = BSC ? w_ref : m_ref;                 // what O is relative to
       const float o_top = BSC ? mxw : mx;
-      const bool move = o_top > o_ref + kRescaleLog2;
+      const float o_new = o_top - kWeightHeadLog2;
+      const bool move = o_new > o_ref + kRescaleLog2;
       const bool scales_o = move && o_ref != -INFINITY;
-      const float alpha = scales_o ? ex2_approx(o_ref - o_top) : 1.f;
+      const float alpha = scales_o ? ex2_approx(o_ref - o_new) : 1.f;
       float l_alpha = alpha;
       if constexpr (BSC) {
         const bool moves = mx > m_ref + kRescaleLog2;
         l_alpha = moves && m_ref != -INFINITY ? ex2_approx(m_ref - mx) : 1.f;
         if (moves) m_ref = mx;
       }
-      if (move) o_ref = o_top;
+      if (move) o_ref = o_new;
       if (j > 0 && __any_sync(0xffffffffu, scales_o)) {
         // O must hold every earlier tile of this group before it is scaled
         wait(&o_bar[grp][(j - 1) % NSB], ((j - 1) / NSB) & 1);

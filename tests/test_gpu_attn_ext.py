@@ -237,6 +237,44 @@ def test_decode_block_scales_far_apart():
     assert ref0.out.isfinite().all()
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(kv="head"), dict(kv="same", dtype="f16", spread=1),
+                                dict(d=256), dict(d=64, bs=64)])
+def test_small_weights_where_the_largest_meet_zeros(kw):
+    # A steep bias: weights fall by 2^-1 a key, and V is 0 for the last 18 keys of a row, so what
+    # is left has weights from 2^-18 on. The largest weight is held as 2^7 or more, so one is off by
+    # 2^-11 of itself or, below f16's normal range (2^-14 against 2^7), by half of its
+    # subnormal step 2^-24: 2^-32 of the largest weight, for each key. (Keys more than 40
+    # back weigh less than 2^-40 each, 300 of them, and may be lost.) With block scales what is
+    # held is the weight times the V scale 2^ev of its block: 2^-32 of the largest
+    # of those, which in units of a key's own weight is at most 2^(largest ev - its ev) more.
+    seqs = [(300, 1), (70, 1), (41, 1)]
+    for lens, run in ((seqs, "decode"), ([(299, 2), (69, 2), (40, 2)], "prefill")):
+        c = Case(21, lens, qsize=0.1, alibi=True, **kw)
+        c.slopes = torch.full_like(c.slopes, 0.6931)
+        bs, hkv = c.v.shape[2], c.v.shape[1]
+        near = torch.zeros(c.q.shape, dtype=torch.float64, device="cuda")
+        for n, (p, q) in enumerate(lens):
+            for j in range(p + q - 18, p + q):
+                c.v[c.tables[n, j // bs].long(), :, j % bs] = 0
+            j = torch.arange(p + q - 41, p + q, device="cuda")
+            block = c.tables[n, j // bs].long()
+            vs = c.vs if c.vs is None or c.vs.dim() == 1 else c.vs[block]
+            v = R.values(c.v[block], vs)[torch.arange(41, device="cuda"), :, j % bs].abs()
+            if c.vs is not None and c.vs.dim() == 2:
+                ev = c.vs[block].double()
+                v = v * torch.exp2(ev.amax(0) - ev)[..., None]
+            near[int(c.cu[n]):int(c.cu[n + 1])] = v.sum(0).repeat_interleave(c.q.shape[1] // hkv, 0)
+        out, _ = getattr(c, run)()
+        ok()
+        ref = c.want()
+        err = (out.double() - ref.out).abs()
+        tol = R.tolerance(ref, c.q.dtype, c.p_dtype) - 2.0 ** -24 + 2.0 ** -32 * near + 2.0 ** -31
+        assert ref.mass.max() < 2.0 ** -11          # nothing but small weights is left
+        if c.q.dtype == torch.float16:               # f16 outputs that small are subnormal
+            tol = tol + 2.0 ** -25
+        assert (err <= tol).all()
+
+
 def test_nan_scale_reaches_its_sequence_alone():
     c = Case(9, [(99, 1), (60, 1)])
     ref = c.want()
