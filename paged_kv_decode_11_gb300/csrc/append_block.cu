@@ -21,22 +21,23 @@
 // consecutive rows (a run of at most BS), so a run, not a token, is the unit:
 // its first row (the leader) starts a sequence's chunk or a block. A CTA takes
 // `window` consecutive rows and one KV head and does the runs whose leaders
-// lie among its rows; its first 128 threads do the keys, the other 128 the
-// values. A group holds 4 x 16 elements of the run per thread in registers from
-// the maximum to the codes; of a longer run (64 tokens at head_dim 256) what
-// was not kept is loaded and rotated again. No two CTAs touch one block and
+// lie among its rows; half of its threads do the keys, the other half the
+// values. A group holds 2 x 16 elements of the run per thread in registers from
+// the maximum to the codes; of a longer run (more than 32 tokens at head_dim 128)
+// what was not kept is loaded and rotated again (holding 4 x 16 spilled registers
+// and left room for fewer CTAs: 2,039 tokens of 24 / 8 heads 14.9 us, 13.2 with 2). No two CTAs touch one block and
 // head, so nothing is atomic and the result does not depend on scheduling. The
-// queries follow in the same grid: a CTA takes a few rows, a thread keeps the
+// queries follow in the same grid: one warp or a few take a row, a thread keeps the
 // angles of its 16 dims and goes over the row's heads.
 //
 // Bound: bytes (16-bit rows in, 8-bit codes out, queries in and out) when the call is
 // long: 7 chunks of 150 to 2,100 tokens, 28 / 4 heads, D = 128, f16, half of each head
-// rotated: 139 MB in 36.5 us, 3.8 TB/s (a plain copy of its queries alone, 113 MB, takes
+// rotated: 139 MB in 35 us, 4.0 TB/s (a plain copy of its queries alone, 113 MB, takes
 // 36.9; 41.6 us with a warp's loads waiting for the stores before them, 91 with a
 // CTA per row and doubles for the undecided sums). For the tokens of a decode batch
 // the chain of loads before the first store (sequence, block id, scale) is what
 // takes the time, so everything that can be addressed without them is loaded first:
-// 128 tokens of 32 / 8 heads 5.5 us, one token 3.2.
+// 128 tokens of 32 / 8 heads 5.5 us, one token 2.9.
 #include "block_scale.cuh"
 #include "f32x2.cuh"
 #include "rope.cuh"
@@ -47,9 +48,7 @@ namespace {
 
 // A CTA has GROUP threads on the keys of a run and GROUP on its values.
 constexpr int kShortGroup = 32, kLongGroup = 128;
-constexpr int kKeep = 4;                   // items (16 elements) a thread keeps of a run
-// Warps that share a row's query heads: four for few rows, one for many.
-constexpr int query_slices(int group) { return group == kLongGroup ? 1 : 4; }
+constexpr int kKeep = 2;                   // items (16 elements) a thread keeps of a run
 
 // The row's sequence n, its position and the rows of its chunk; n = -1 for rows
 // that no sequence owns or whose sequence is not valid (flagged elsewhere).
@@ -63,36 +62,48 @@ __device__ __forceinline__ bool seq_valid(const AppendBlockParams& p, int q0, in
          (p.cos_sin == nullptr || ctx <= p.max_position);
 }
 
+// Every lane of a warp, each for a row of its own (or -1). Few sequences are looked
+// up at once, in one round trip: a lane reads the offsets and the length of one.
 __device__ __forceinline__ RowPlace place_of(const AppendBlockParams& p, int row) {
-  RowPlace r{-1, 0, 0, 0};
-  // a decode batch has row n in sequence n: one round trip to see it
-  int n = row, q0 = -1, q1 = -1, ctx = 0;
-  if (row < p.num_seqs) {
-    q0 = p.cu_q_lens[row];
-    q1 = p.cu_q_lens[row + 1];
-    ctx = p.seq_lens[row];
-  }
-  if (!(q0 <= row && row < q1)) {
-    // the last n with cu_q_lens[n] <= row
-    int lo = 0, hi = p.num_seqs + 1;       // cu[lo] <= row (if any), cu[hi] > row
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.cu_q_lens[mid] <= row) lo = mid;
-      else hi = mid;
+  int n, q0, q1, ctx;
+  if (p.num_seqs < 32) {
+    const int lane = threadIdx.x & 31;
+    const int cu = lane <= p.num_seqs ? p.cu_q_lens[lane] : 0x7FFFFFFF;
+    const int len = lane < p.num_seqs ? p.seq_lens[lane] : 0;
+    n = -1;                                // the last n with cu_q_lens[n] <= row
+    for (int k = 0; k <= p.num_seqs; ++k) n += __shfl_sync(0xffffffffu, cu, k) <= row ? 1 : 0;
+    const int at = max(n, 0);
+    q0 = __shfl_sync(0xffffffffu, cu, at);
+    q1 = __shfl_sync(0xffffffffu, cu, (at + 1) & 31);
+    ctx = __shfl_sync(0xffffffffu, len, at);
+  } else {
+    // a decode batch has row n in sequence n: one round trip to see it
+    n = row;
+    q0 = q1 = -1;
+    ctx = 0;
+    if (row >= 0 && row < p.num_seqs) {
+      q0 = p.cu_q_lens[row];
+      q1 = p.cu_q_lens[row + 1];
+      ctx = p.seq_lens[row];
     }
-    n = lo;
-    if (n >= p.num_seqs) return r;
-    q0 = p.cu_q_lens[n];
-    q1 = p.cu_q_lens[n + 1];
-    if (row < q0 || row >= q1) return r;
-    ctx = p.seq_lens[n];
+    if (!(q0 <= row && row < q1)) {
+      int lo = 0, hi = p.num_seqs + 1;     // cu[lo] <= row (if any), cu[hi] > row
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu_q_lens[mid] <= row) lo = mid;
+        else hi = mid;
+      }
+      n = lo;
+      if (n < p.num_seqs) {
+        q0 = p.cu_q_lens[n];
+        q1 = p.cu_q_lens[n + 1];
+        ctx = p.seq_lens[n];
+      }
+    }
   }
-  if (!seq_valid(p, q0, q1, ctx)) return r;
-  r.n = n;
-  r.q0 = q0;
-  r.ctx = ctx;
-  r.pos = ctx - (q1 - row);
-  return r;
+  if (n < 0 || n >= p.num_seqs || row < q0 || row >= q1 || !seq_valid(p, q0, q1, ctx))
+    return RowPlace{-1, 0, 0, 0};
+  return RowPlace{n, ctx - (q1 - row), q0, ctx};
 }
 
 // Largest finite magnitude (bits) of the 16-bit values of a word pair by pair.
@@ -221,7 +232,7 @@ __device__ __forceinline__ Pair8 load_item(const uint16_t* row, int j, int rot) 
 template <bool BF16, bool NEOX, int GROUP>
 __global__ void __launch_bounds__(2 * GROUP, GROUP == kLongGroup ? 3 : 8)
     append_block_kernel(const __grid_constant__ AppendBlockParams p) {
-  constexpr int kGroup = GROUP, kThreads = 2 * GROUP, kSlices = query_slices(GROUP);
+  constexpr int kGroup = GROUP, kThreads = 2 * GROUP;
   // a decode launched behind this kernel may become resident now; it waits
   // for this grid to finish before it reads anything
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -242,8 +253,8 @@ __global__ void __launch_bounds__(2 * GROUP, GROUP == kLongGroup ? 3 : 8)
     const int64_t stride = (int64_t)p.Hkv << p.d_log2;
     // a lane looks one row up; then the rows that lead a run are taken in turn
     const int lane = tid & 31;
-    RowPlace mine{-1, 0, 0, 0};
-    if (lane < p.window && r0 + lane < p.rows) mine = place_of(p, r0 + lane);
+    const RowPlace mine =
+        place_of(p, lane < p.window && r0 + lane < p.rows ? r0 + lane : -1);
     uint32_t leaders = __ballot_sync(
         0xffffffffu, mine.n >= 0 && (r0 + lane == mine.q0 || (mine.pos & (bs - 1)) == 0));
     while (leaders != 0u) {                        // the same for every warp of the CTA
@@ -350,14 +361,15 @@ __global__ void __launch_bounds__(2 * GROUP, GROUP == kLongGroup ? 3 : 8)
   if (p.query_out == nullptr) return;
   const int lane = tid & 31;
   const int64_t task = (int64_t)cta * (kThreads / 32) + (tid >> 5);
-  const int row = (int)(task / kSlices), slice = (int)(task % kSlices);
+  const int row = (int)(task >> p.slices_log2), slices = 1 << p.slices_log2;
+  const int slice = (int)task & (slices - 1);
   if (row >= p.rows) return;
   const int64_t o = (int64_t)row * p.Hq << p.d_log2;
   const uint16_t* q = static_cast<const uint16_t*>(p.query) + o;
   uint16_t* out = static_cast<uint16_t*>(p.query_out) + o;
   // the rotated items: lane = (head, item j) with as many heads at a time as fit, j
   // and its angles staying; the warp's heads advance by `step`
-  const int R = p.rot / 16, per = 32 / R, step = per * kSlices;
+  const int R = p.rot / 16, per = 32 / R, step = per * slices;
   const int j = lane % R;
   const int h_end = lane < per * R ? p.Hq : 0;
   int h0 = slice * per + lane / R;
@@ -381,8 +393,8 @@ __global__ void __launch_bounds__(2 * GROUP, GROUP == kLongGroup ? 3 : 8)
   auto load_rest = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < C; ++u)
-      if (i0 + 32 * kSlices * u < n_rest)
-        rest[u] = *reinterpret_cast<const uint4*>(q + rest_at(i0 + 32 * kSlices * u));
+      if (i0 + 32 * slices * u < n_rest)
+        rest[u] = *reinterpret_cast<const uint4*>(q + rest_at(i0 + 32 * slices * u));
   };
   load_rest(slice * 32 + lane);
   const RowPlace at = place_of(p, row);
@@ -391,9 +403,9 @@ __global__ void __launch_bounds__(2 * GROUP, GROUP == kLongGroup ? 3 : 8)
   for (int i0 = slice * 32 + lane; i0 < n_rest;) {
 #pragma unroll
     for (int u = 0; u < C; ++u)
-      if (i0 + 32 * kSlices * u < n_rest)
-        *reinterpret_cast<uint4*>(out + rest_at(i0 + 32 * kSlices * u)) = rest[u];
-    i0 += 32 * kSlices * C;
+      if (i0 + 32 * slices * u < n_rest)
+        *reinterpret_cast<uint4*>(out + rest_at(i0 + 32 * slices * u)) = rest[u];
+    i0 += 32 * slices * C;
     load_rest(i0);
   }
   int a, b;
@@ -436,16 +448,24 @@ pkv_status launch_append_block(const AppendBlockParams& params, pkv_dtype src_dt
   AppendBlockParams p = params;
   if (p.rows == 0) return PKV_OK;
   // rows per cache-write CTA: about as many as a run has on average (at most
-  // rows / BS + num_seqs rows lead one), so that a CTA meets one leader, not
-  // none (a CTA spent finding that out) and not several (done in turn)
+  // rows / BS + num_seqs rows lead one), rounded up, so that few CTAs meet no leader
+  // (spent finding that out) and few meet several (done in turn)
   const int64_t leaders = ((int64_t)p.rows >> p.bs_log2) + p.num_seqs;
   p.window = 1;
-  while (p.window < 32 && 2 * p.window * leaders <= p.rows) p.window *= 2;
+  while (p.window < 32 && p.window * leaders < p.rows) p.window *= 2;
   // a warp on the keys of a run while runs may be single tokens, four for chunks
   const bool is_short = p.window == 1;
   const int group = is_short ? kShortGroup : kLongGroup;
   const int64_t kv = (((int64_t)p.rows + p.window - 1) / p.window) * p.Hkv;
-  const int64_t warps = (int64_t)p.rows * query_slices(group), wpc = 2 * group / 32;
+  // warps per row of queries: enough that few rows still fill the GPU, while each has
+  // two heads' worth of items to do (297 rows of 56 heads: one warp each
+  // 12.1 us, eight 5.5)
+  const int per = p.cos_sin == nullptr ? 1 : 32 / (p.rot / 16);
+  p.slices_log2 = 0;
+  while (p.slices_log2 < 3 && ((int64_t)p.rows << p.slices_log2) < 4096 &&
+         (per << p.slices_log2) < p.Hq)
+    ++p.slices_log2;
+  const int64_t warps = (int64_t)p.rows << p.slices_log2, wpc = 2 * group / 32;
   const int64_t q = p.query_out == nullptr ? 1 : (warps + wpc - 1) / wpc;
   if (kv + q > 0x7FFFFFFF) return PKV_ERR_INVALID_ARG;
   p.kv_ctas = (unsigned int)kv;

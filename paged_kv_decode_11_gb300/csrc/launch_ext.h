@@ -27,6 +27,7 @@ struct AppendBlockParams {
   int bs_log2;                  // log2(block_size), 4 to 6
   int window;                   // rows per cache-write CTA (at most 32)
   unsigned int kv_ctas;         // cache-write CTAs, the first of the grid
+  int slices_log2;              // log2 of the warps per row of queries
 };
 
 // Launches nothing for rows = 0; validates nothing (the entry point does).
