@@ -84,22 +84,31 @@ __device__ __forceinline__ float softcap_log2(float x, float cap_log2, float two
   return fmaf(-2.f * cap_log2, r, cap_log2);
 }
 
-// softcap_log2 of N scores of one row, the whole warp with its rows at once.
-// Scores seldom leave (-softcap, softcap), and there tanh(y) = y P(y^2) with P of
-// degree 6 is off by less than 1.3e-7 (the Chebyshev interpolant of
-// tanh(sqrt t) / sqrt t on [0, 1], evaluated in fp32): five packed operations a
-// score, where the general form takes two of the special-function unit's, which
-// the softmax itself keeps busy. A warp with a larger score takes that one.
+// softcap_log2 of the N scores of a thread's row, of which it sees first..last; the
+// others (left-over bytes, maybe) become 0. Scores seldom leave (-softcap, softcap),
+// and there tanh(y) = y P(y^2) with P of degree 6 is off by less than 1.3e-7 (the
+// Chebyshev interpolant of tanh(sqrt t) / sqrt t on [0, 1], evaluated in fp32): five
+// packed operations a score, where the general form takes two of the special-function
+// unit's, which the softmax itself keeps busy. A row with a larger score takes that
+// one. The choice is the row's own, so that its bits depend neither on keys it does
+// not see nor on the warp's other rows (the warp choosing for all of its rows, unseen
+// keys included, took 103 us on the capped window where this takes 107).
 template <int N>
-__device__ __forceinline__ void softcap_log2_row(float (&x)[N], float cap_log2,
-                                                 float two_over_cap) {
+__device__ __forceinline__ void softcap_log2_row(float (&x)[N], int first, int last,
+                                                 float cap_log2, float two_over_cap) {
   constexpr float kP[7] = {0.99999994f, -0.33332857f, 0.13325398f, -0.053465176f,
                            0.02030552f, -0.0062170699f, 0.0010455536f};
   const float inv = two_over_cap * (0.5f * kLn2);       // 1 / cap_log2
+  if (first > 0 || last < N - 1) {
+    const unsigned span = (unsigned)(last - first);
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      if ((unsigned)(c - first) > span) x[c] = 0.f;
+  }
   float top = 0.f;
 #pragma unroll
   for (int c = 0; c < N; ++c) top = fmaxf(top, fabsf(x[c]));
-  if (__all_sync(0xffffffffu, top * inv <= 1.f)) {
+  if (top * inv <= 1.f) {
     const f2 i2 = pack_f2(inv, inv);
 #pragma unroll
     for (int c = 0; c < N; c += 2) {

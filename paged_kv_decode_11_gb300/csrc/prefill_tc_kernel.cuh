@@ -904,7 +904,8 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
           // the scores themselves, in log2 units
 #pragma unroll
           for (int c = 0; c < CH; ++c) x[c] *= BSC ? kf[c / kBS] : sl2;
-          if (ep.cap_log2 != 0.f) softcap_log2_row(x, ep.cap_log2, ep.two_over_cap);
+          if (ep.cap_log2 != 0.f)
+            softcap_log2_row(x, lo - k0, last - k0, ep.cap_log2, ep.two_over_cap);
           if (ep.slopes != nullptr) {
             const float d0 = (float)(k0 - pos);
 #pragma unroll

@@ -385,6 +385,36 @@ def test_largest_window_sees_everything(kw):
     ok()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(kv="same", spread=1, softcap=30.0), dict(kv="same", spread=1, softcap=3.0, window=200),
+    dict(kv="same", spread=1, softcap=3.0, d=256, dtype="f16"), dict(kv="head", softcap=3.0, d=64),
+    dict(softcap=3.0, alibi=True), dict(softcap=30.0, d=64, bs=32), dict(), dict(window=70),
+    dict(kv="same", spread=1, alibi=True)])
+def test_prefill_rows_do_not_depend_on_keys_they_do_not_see(kw):
+    # the last 20 tokens' keys and values change, and the slots behind them: not one bit of the
+    # rows before them does
+    seqs = [(300, 100), (0, 70), (650, 45), (33, 21)]
+    c = Case(137, seqs, **kw)
+    out, lse = c.prefill()
+    ok()
+    bs = c.k.shape[2]
+    big = torch.tensor(64.0).to(c.k.dtype).cuda()
+    for i, (p, q) in enumerate(seqs):
+        for j in range(p + q - 20, -(-(p + q) // bs) * bs):
+            b = int(c.tables[i, j // bs])
+            c.k[b, :, j % bs, ::2] = big
+            c.k[b, :, j % bs, 1::2] = big / 2 if c.k.dtype != torch.float8_e4m3fn else big
+            c.v[b, :, j % bs] = big
+    out2, lse2 = c.prefill()
+    ok()
+    at = 0
+    for p, q in seqs:
+        rows = slice(at, at + q - 20)
+        assert torch.equal(out[rows], out2[rows]) and torch.equal(lse[rows], lse2[rows])
+        assert not torch.equal(out[at + q - 20:at + q], out2[at + q - 20:at + q])
+        at += q
+
+
 def test_prefill_bad_sequences():
     c = Case(13, [(50, 10), (3, 20), (70, 8)])
     ref = c.want()
