@@ -4,6 +4,17 @@
 
 namespace pkv {
 
+// SMs of device `dev`, read once; 0 on failure.
+static int prefill_tc_sms(int dev) {
+  static std::atomic<int> sms[64];
+  int n = sms[dev].load();
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    sms[dev].store(n);
+  }
+  return n;
+}
+
 // One CTA per query tile when that fills at least half of the GPU (or other
 // work shares it); otherwise a cluster of two per tile, each taking half of
 // the key tiles. Beside a decode grid (may_split false), the 64-key tiles.
@@ -20,10 +31,10 @@ static pkv_status launch_prefill_tc_t(const PrefillParams& p, const CUtensorMap&
   q.q_tile = kTcRows / p.G;
   const int64_t ctas = (int64_t)((q.max_q_len + q.q_tile - 1) / q.q_tile) * q.Hkv * q.num_seqs;
   if (!may_split)
-    return launch_prefill_tc_s<D, KV, QBF16, 1, false, kTcPlain>(q, tmQ, tmK, tmV, stream, dev);
+    return PrefillTcLaunch<D, KV, QBF16, 1, false, kTcPlain>::launch(q, tmQ, tmK, tmV, stream, dev);
   if (2 * ctas <= n_sms)
-    return launch_prefill_tc_s<D, KV, QBF16, 2, true, kTcPlain>(q, tmQ, tmK, tmV, stream, dev);
-  return launch_prefill_tc_s<D, KV, QBF16, 1, true, kTcPlain>(q, tmQ, tmK, tmV, stream, dev);
+    return PrefillTcLaunch<D, KV, QBF16, 2, true, kTcPlain>::launch(q, tmQ, tmK, tmV, stream, dev);
+  return PrefillTcLaunch<D, KV, QBF16, 1, true, kTcPlain>::launch(q, tmQ, tmK, tmV, stream, dev);
 }
 
 template <int D>

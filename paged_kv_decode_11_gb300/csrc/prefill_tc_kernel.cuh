@@ -28,8 +28,8 @@
 //   reference max that moves only when the row max grows by more than 2^8,
 //   so O in TMEM is rescaled rarely. At the end the groups' (O, max, sum)
 //   are merged by log-sum-exp, the same softmax. When a small grid leaves
-//   SMs idle, a cluster of two CTAs splits each tile's keys and the two
-//   merge the same way through distributed shared memory.
+//   SMs idle, a cluster of two CTAs (MODE: up to eight) splits each tile's keys
+//   and they merge the same way through distributed shared memory.
 //
 // Shared memory: Q [D/64][128 rows][128 B], then NST stages of
 // K [D/64][4 pages][16 rows][128 B], NST stages of V (same), then two P
@@ -52,6 +52,7 @@
 //   rewritten once, in registers, between tensor memory and the maximum.
 #pragma once
 #include <cuda.h>
+#include <algorithm>
 #include <type_traits>
 #include "block_scale.cuh"
 #include "common.cuh"
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   __shared__ uint64_t stg_k[NSS * Cfg::PK], stg_v[NSS * Cfg::PV];
   // per softmax group g and buffer b: S ready, P written, P.V done
   __shared__ uint64_t s_bar[NG][NSB], o_bar[NG][NSB], p_bar[NG][NSB];
-  __shared__ uint64_t ready_bar, recv_bar;              // cluster hand-off (SPLIT == 2)
+  __shared__ uint64_t ready_bar, recv_bar;              // cluster hand-off (SPLIT > 1)
   __shared__ uint64_t done_bar;                         // PTM: every MMA of the CTA is done
   __shared__ uint64_t q_bar;                            // 16-bit cache: the query tile landed
   __shared__ uint32_t tmem_base;
@@ -493,8 +494,8 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
           mbar_init(&o_bar[g][b], 1);
           mbar_init(&p_bar[g][b], kTcRows);             // every thread of the group
         }
-      mbar_init(&ready_bar, 1);
-      mbar_init(&recv_bar, NG * kTcRows);
+      mbar_init(&ready_bar, SPLIT > 1 ? SPLIT - 1 : 1);
+      mbar_init(&recv_bar, (SPLIT > 1 ? SPLIT - 1 : 1) * NG * kTcRows);
       mbar_init(&done_bar, 1);
       mbar_init(&q_bar, 1);
       fence_barrier_init();
@@ -1088,10 +1089,13 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   const float w0 = f0, w1 = f1;
 
   // CTA `split` of the cluster finishes columns [split CW, (split + 1) CW),
-  // group g of it the part [g QW, (g + 1) QW) of those.
+  // group g of it the part [g QW, (g + 1) QW) of those (or group 0 all of them,
+  // where a part would be less than tensor memory gives at once).
   constexpr int CW = D / SPLIT;
-  constexpr int QW = CW / NG;
+  constexpr int PARTS = CW / NG >= 16 ? NG : 1;
+  constexpr int QW = CW / PARTS;
   constexpr int CH = QW < 32 ? QW : 32;                 // TMEM columns per load
+  const bool has_part = PARTS == NG || grp < PARTS;
   const int mycol = split * CW + grp * QW;
   // combined O of this CTA for columns [c, c + CH)
   auto combined = [&](int c, float (&f)[CH]) {
@@ -1106,51 +1110,78 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
     }
   };
 
-  // SPLIT == 2: each CTA hands the other the combined O of the other's
-  // columns, with its M and sum, into the other's K ring (drained once that
-  // CTA's last P.V, and so its last S, is done):
+  // SPLIT > 1: each CTA hands every other the combined O of the other's
+  // columns, with its M and sum, into a place of its own in the other's K and V
+  // rings (drained once that CTA's last P.V, and so its last S, is done):
   //   O as [CW / 4][128 rows] float4 (a warp's rows side by side, no bank
-  //   conflicts), then (M, sum) as [128 rows] float2.
-  float M_o = -INFINITY, L_o = 0.f, W_o = -INFINITY;
-  const uint32_t recv_rows = sKV;
-  const uint32_t recv_ml = sKV + kTcRows * CW * 4;
-  if constexpr (SPLIT > 1) {
-    const uint32_t other = (uint32_t)(split ^ 1);
-    cluster_wait();                                     // the other CTA's barriers are set up
-    if (tid == 0) mbar_arrive_remote(cluster_map(smem_u32(&ready_bar), other));
-    if (!mbar_wait_cluster(&ready_bar, 0)) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
-    const uint32_t dst = cluster_map(recv_rows, other) + r * 16;
+  //   conflicts), then all the (M, sum) as [128 rows] each.
+  constexpr int NO = SPLIT > 1 ? SPLIT - 1 : 1;         // other CTAs
+  constexpr uint32_t O_BYTES = kTcRows * CW * 4;
+  Share theirs[NO];
 #pragma unroll
-    for (int c0 = 0; c0 < QW; c0 += CH) {
-      float f[CH];
-      combined((int)other * CW + grp * QW + c0, f);
-#pragma unroll
-      for (int c = 0; c < CH; c += 4)
-        st_cluster_v4(dst + ((grp * QW + c0 + c) / 4) * (kTcRows * 16), f[c], f[c + 1],
-                      f[c + 2], f[c + 3]);
-    }
-    if (grp == 0) {
-      if constexpr (BSC) st_cluster_v4(cluster_map(recv_ml, other) + r * 16, M, Lc, W, 0.f);
-      else st_cluster_v2(cluster_map(recv_ml, other) + r * 8, M, Lc);
-    }
-    mbar_arrive_remote(cluster_map(smem_u32(&recv_bar), other));
-    if (!mbar_wait_cluster(&recv_bar, 0)) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
-    const Share ml = reinterpret_cast<const Share*>(basep + (recv_ml - base))[r];
-    M_o = ml.x;
-    L_o = ml.y;
-    if constexpr (BSC) W_o = ml.z;
+  for (int o = 0; o < NO; ++o) {
+    theirs[o].x = -INFINITY;
+    theirs[o].y = 0.f;
+    if constexpr (BSC) theirs[o].z = -INFINITY;
   }
-  // with the other CTA's share: M2 = max(M, M_o), O = O 2^(M - M2) + O_o 2^(M_o - M2)
-  const float M2 = fmaxf(M, M_o);
+  const uint32_t recv_rows = sKV;
+  const uint32_t recv_ml = sKV + NO * O_BYTES;
+  if constexpr (SPLIT > 1) {
+    cluster_wait();                                     // the others' barriers are set up
+    if (tid == 0)
+      for (int o = 1; o < SPLIT; ++o)
+        mbar_arrive_remote(cluster_map(smem_u32(&ready_bar), (uint32_t)(split + o) % SPLIT));
+    if (!mbar_wait_cluster(&ready_bar, 0)) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+#pragma unroll
+    for (int o = 1; o < SPLIT; ++o) {
+      const uint32_t other = (uint32_t)(split + o) % SPLIT;
+      const uint32_t place = SPLIT - 1 - o;             // this CTA's place there
+      const uint32_t dst = cluster_map(recv_rows + place * O_BYTES, other) + r * 16;
+      if (has_part) {
+#pragma unroll
+        for (int c0 = 0; c0 < QW; c0 += CH) {
+          float f[CH];
+          combined((int)other * CW + grp * QW + c0, f);
+#pragma unroll
+          for (int c = 0; c < CH; c += 4)
+            st_cluster_v4(dst + ((grp * QW + c0 + c) / 4) * (kTcRows * 16), f[c], f[c + 1],
+                          f[c + 2], f[c + 3]);
+        }
+      }
+      if (grp == 0) {
+        const uint32_t at = cluster_map(recv_ml + (place * kTcRows + r) * sizeof(Share), other);
+        if constexpr (BSC) st_cluster_v4(at, M, Lc, W, 0.f);
+        else st_cluster_v2(at, M, Lc);
+      }
+      mbar_arrive_remote(cluster_map(smem_u32(&recv_bar), other));
+    }
+    if (!mbar_wait_cluster(&recv_bar, 0)) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+#pragma unroll
+    for (int o = 0; o < NO; ++o)
+      theirs[o] = reinterpret_cast<const Share*>(basep + (recv_ml - base))[o * kTcRows + r];
+  }
+  // with the other CTAs' shares: M2 = max(M, M_o), O = O 2^(M - M2) + sum O_o 2^(M_o - M2)
+  float M2 = M;
+#pragma unroll
+  for (int o = 0; o < NO; ++o) M2 = fmaxf(M2, theirs[o].x);
   float a0 = M == -INFINITY ? 0.f : SPLIT == 1 ? 1.f : ex2_approx(M - M2);
-  float a1 = M_o == -INFINITY ? 0.f : ex2_approx(M_o - M2);
-  const float L2 = Lc * a0 + L_o * a1;
+  float ao[NO];
+  float L2 = Lc * a0;
+#pragma unroll
+  for (int o = 0; o < NO; ++o) {
+    ao[o] = theirs[o].x == -INFINITY ? 0.f : ex2_approx(theirs[o].x - M2);
+    L2 += theirs[o].y * ao[o];
+  }
   float inv = L2 > 0.f ? (KV8 && !BSC ? p.v_scales[h] : 1.f) / L2 : 0.f;
   if constexpr (BSC) {
     // O 2^W against its sum L2 2^M2
-    const float W2 = fmaxf(W, W_o);
+    float W2 = W;
+#pragma unroll
+    for (int o = 0; o < NO; ++o) W2 = fmaxf(W2, theirs[o].z);
     a0 = W == -INFINITY ? 0.f : SPLIT == 1 ? 1.f : ex2_approx(W - W2);
-    a1 = W_o == -INFINITY ? 0.f : ex2_approx(W_o - W2);
+#pragma unroll
+    for (int o = 0; o < NO; ++o)
+      ao[o] = theirs[o].z == -INFINITY ? 0.f : ex2_approx(theirs[o].z - W2);
     inv *= W2 == -INFINITY ? 0.f : exp2f(W2 - M2);
   }
   const float4* orecv = reinterpret_cast<const float4*>(basep + (recv_rows - base)) + r;
@@ -1158,17 +1189,25 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
                                                     (rvalid ? hq : 0)) * D;
 #pragma unroll
   for (int c0 = 0; c0 < QW; c0 += CH) {
+    if (!has_part) break;
     float f[CH];
     combined(mycol + c0, f);
     if (rvalid) {
 #pragma unroll
       for (int c = 0; c < CH; c += 4) {
-        float4 of = make_float4(0.f, 0.f, 0.f, 0.f);
-        if constexpr (SPLIT > 1) of = orecv[((grp * QW + c0 + c) / 4) * kTcRows];
-        f[c] = (f[c] * a0 + of.x * a1) * inv;
-        f[c + 1] = (f[c + 1] * a0 + of.y * a1) * inv;
-        f[c + 2] = (f[c + 2] * a0 + of.z * a1) * inv;
-        f[c + 3] = (f[c + 3] * a0 + of.w * a1) * inv;
+        float s[4] = {f[c] * a0, f[c + 1] * a0, f[c + 2] * a0, f[c + 3] * a0};
+        if constexpr (SPLIT > 1) {
+#pragma unroll
+          for (int o = 0; o < NO; ++o) {
+            const float4 of = orecv[(o * (CW / 4) + (grp * QW + c0 + c) / 4) * kTcRows];
+            s[0] += of.x * ao[o];
+            s[1] += of.y * ao[o];
+            s[2] += of.z * ao[o];
+            s[3] += of.w * ao[o];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[c + k] = s[k] * inv;
       }
 #pragma unroll
       for (int c = 0; c < CH / 8; ++c) {
@@ -1186,82 +1225,125 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   if (warp == 0) tc::dealloc(tm, Cfg::TMEM_COLS);
 }
 
+// One instance of the kernel and its launches.
 template <int D, int KV, bool QBF16, int SPLIT, bool ALONE, int MODE>
-static pkv_status launch_prefill_tc_s(const PrefillTcParams<MODE>& ep, const CUtensorMap& tmQ,
-                                      const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                      cudaStream_t stream, int dev) {
-  constexpr bool KV8 = KV == KV_E4M3;
+struct PrefillTcLaunch {
+  static constexpr bool KV8 = KV == KV_E4M3;
   // ring stages: the 128-key tiles (P in tensor memory) take 3 of 32 KB at
   // D = 128 and 6 of 16 KB at D = 64, less the staging of an E4M3 cache 2 and 4;
   // the 64-key tiles of E4M3 caches and D = 256 take 2, the rest 4
-  constexpr bool WIDE = PrefillTcCfg<D, 2, KV8, ALONE, MODE>::WIDE;
-  constexpr int NST = WIDE ? (KV8 ? (D == 128 ? 2 : 4) : D == 128 ? 3 : 6)
-                           : ((D > 128 || KV8) ? 2 : 4);
+  static constexpr bool WIDE = PrefillTcCfg<D, 2, KV8, ALONE, MODE>::WIDE;
+  static constexpr int NST = WIDE ? (KV8 ? (D == 128 ? 2 : 4) : D == 128 ? 3 : 6)
+                                  : ((D > 128 || KV8) ? 2 : 4);
   using Cfg = PrefillTcCfg<D, NST, KV8, ALONE, MODE>;
   static_assert(Cfg::SMEM_BYTES + 1280 <= 227 * 1024, "shared memory (dynamic + static)");
-  static_assert(SPLIT == 1 || kTcRows * (D / SPLIT) * 4 + kTcRows * 16 <= 2 * Cfg::RING_BYTES,
-                "the other CTA's rows must fit in the ring");
-  auto kern = prefill_tc_kernel<D, KV, QBF16, NST, SPLIT, ALONE, MODE>;
-  static std::atomic<bool> attr_set[64];  // per device; the call is idempotent
-  if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg::SMEM_BYTES) != cudaSuccess)
-      return PKV_ERR_CUDA;
-    if constexpr (Cfg::REALLOC) {
-      // a register raise waits for registers the CTA does not have unless
-      // the launch allocation covers every warpgroup's count: never launch then
-      cudaFuncAttributes fa{};
-      if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
-      if ((int64_t)fa.numRegs * Cfg::THREADS < Cfg::REG_TOTAL) return PKV_ERR_UNSUPPORTED;
+  static_assert(SPLIT == 1 || (SPLIT - 1) * (kTcRows * (D / SPLIT) * 4 + kTcRows * 16) <=
+                                  2 * Cfg::RING_BYTES,
+                "the other CTAs' rows must fit in the rings");
+
+  // The kernel's attributes on the current device `dev`, set once.
+  static pkv_status prepare(int dev) {
+    auto kern = prefill_tc_kernel<D, KV, QBF16, NST, SPLIT, ALONE, MODE>;
+    static std::atomic<bool> attr_set[64];  // per device; the call is idempotent
+    if (!attr_set[dev]) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Cfg::SMEM_BYTES) != cudaSuccess)
+        return PKV_ERR_CUDA;
+      if constexpr (Cfg::REALLOC) {
+        // a register raise waits for registers the CTA does not have unless
+        // the launch allocation covers every warpgroup's count: never launch then
+        cudaFuncAttributes fa{};
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
+        if ((int64_t)fa.numRegs * Cfg::THREADS < Cfg::REG_TOTAL) return PKV_ERR_UNSUPPORTED;
+      }
+      attr_set[dev] = true;
     }
-    attr_set[dev] = true;
+    return PKV_OK;
   }
-  const PrefillParams& q = prefill_base(ep);
-  const int tiles = (q.max_q_len + q.q_tile - 1) / q.q_tile;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = SPLIT;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * SPLIT, q.Hkv, q.num_seqs);
-  cfg.blockDim = dim3(Cfg::THREADS);
-  cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tmQ, tmK, tmV, ep) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
-}
 
-// SMs of device `dev`, read once; 0 on failure.
-static int prefill_tc_sms(int dev) {
-  static std::atomic<int> sms[64];
-  int n = sms[dev].load();
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    sms[dev].store(n);
+  static void config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, dim3 grid,
+                     cudaStream_t stream) {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = SPLIT;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(Cfg::THREADS);
+    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
   }
-  return n;
-}
 
-// The _ext calls: one CTA per query tile when that fills at least half of the
-// GPU; otherwise a cluster of two per tile, each taking
-// half of the key tiles.
+  // Clusters that device `dev` holds at once, read once: fewer than its SMs over
+  // SPLIT, as a cluster stays within a GPC. 0 on failure.
+  static int clusters(int dev) {
+    static std::atomic<int> held[64];
+    int n = held[dev];
+    if (n == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr;
+      config(cfg, attr, dim3(SPLIT), nullptr);
+      if (prepare(dev) != PKV_OK ||
+          cudaOccupancyMaxActiveClusters(
+              &n, prefill_tc_kernel<D, KV, QBF16, NST, SPLIT, ALONE, MODE>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();                       // the caller takes another form
+        return 0;
+      }
+      held[dev] = n;
+    }
+    return n;
+  }
+
+  static pkv_status launch(const PrefillTcParams<MODE>& ep, const CUtensorMap& tmQ,
+                           const CUtensorMap& tmK, const CUtensorMap& tmV, cudaStream_t stream,
+                           int dev) {
+    const pkv_status st = prepare(dev);
+    if (st != PKV_OK) return st;
+    const PrefillParams& q = prefill_base(ep);
+    const int tiles = (q.max_q_len + q.q_tile - 1) / q.q_tile;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    config(cfg, attr, dim3(tiles * SPLIT, q.Hkv, q.num_seqs), stream);
+    return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<D, KV, QBF16, NST, SPLIT, ALONE, MODE>, tmQ,
+                              tmK, tmV, ep) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+  }
+};
+
+// The _ext calls: one CTA per query tile, or a cluster of two, four or eight that
+// split its keys: the most of which the device holds all at once with a key tile for
+// every softmax group (the table's width bounds the keys). Measured on 4 rows of 8,000
+// keys, 8 KV heads of 128: two CTAs a tile 59.4 us, four 36.5, eight 26.0; but 38
+// tiles of 4,000 keys, two CTAs each: 40.3 us, and four, which the SMs would hold and
+// the GPCs do not: 52.5.
 template <int D, int KV, bool QBF16, int MODE>
 static pkv_status launch_tc_ext(const PrefillExtParams& ep, const CUtensorMap& tmQ,
                                 const CUtensorMap& tmK, const CUtensorMap& tmV,
                                 cudaStream_t stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_ERR_CUDA;
-  const int n_sms = prefill_tc_sms(dev);
-  if (n_sms == 0) return PKV_ERR_CUDA;
   PrefillExtParams p = ep;
   PrefillParams& q = p.base;
   q.q_tile = kTcRows / q.G;
-  const int64_t ctas = (int64_t)((q.max_q_len + q.q_tile - 1) / q.q_tile) * q.Hkv * q.num_seqs;
-  if (2 * ctas <= n_sms)
-    return launch_prefill_tc_s<D, KV, QBF16, 2, false, MODE>(p, tmQ, tmK, tmV, stream, dev);
-  return launch_prefill_tc_s<D, KV, QBF16, 1, false, MODE>(p, tmQ, tmK, tmV, stream, dev);
+  const int64_t tiles = (int64_t)((q.max_q_len + q.q_tile - 1) / q.q_tile) * q.Hkv * q.num_seqs;
+  int64_t keys = ((int64_t)q.max_blocks * kBS) << q.ppb_shift;
+  if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + q.q_tile);
+  using One = PrefillTcLaunch<D, KV, QBF16, 1, false, MODE>;
+  using Two = PrefillTcLaunch<D, KV, QBF16, 2, false, MODE>;
+  using Four = PrefillTcLaunch<D, KV, QBF16, 4, false, MODE>;
+  const int64_t key_tiles = (keys + One::Cfg::KEYS - 1) / One::Cfg::KEYS;
+  if constexpr (D >= 128) {                             // a share is 16 columns or more
+    using Eight = PrefillTcLaunch<D, KV, QBF16, 8, false, MODE>;
+    if (key_tiles >= 8 * One::Cfg::NG && tiles <= Eight::clusters(dev))
+      return Eight::launch(p, tmQ, tmK, tmV, stream, dev);
+  }
+  if (key_tiles >= 4 * One::Cfg::NG && tiles <= Four::clusters(dev))
+    return Four::launch(p, tmQ, tmK, tmV, stream, dev);
+  if (key_tiles >= 2 * One::Cfg::NG && tiles <= Two::clusters(dev))
+    return Two::launch(p, tmQ, tmK, tmV, stream, dev);
+  return One::launch(p, tmQ, tmK, tmV, stream, dev);
 }
 
 }  // namespace pkv

@@ -335,6 +335,25 @@ def test_prefill_sizes(seqs, kw):
     c.check(got)
 
 
+# few query rows on long contexts: the keys of a query tile are shared out over the CTAs of a
+# cluster, some of which (the short sequences, the windows) get none
+@pytest.mark.parametrize("kw", [
+    dict(), dict(dtype="f16", softcap=20.0, alibi=True), dict(window=1200), dict(window=300),
+    dict(prefix=[2000, 0, 700, 1, 5, 900]), dict(d=64), dict(d=64, alibi=True, bs=32),
+    dict(d=256, hq=3, hkv=1), dict(d=256, softcap=4.0, window=600),
+    dict(kv="head", alibi=True), dict(kv="head", d=64, dtype="f16", window=2100),
+    dict(kv="head", d=256, softcap=30.0), dict(kv="same", spread=1, softcap=30.0),
+    dict(kv="same", spread=1, d=64, dtype="f16", alibi=True),
+    dict(kv="same", spread=1, d=256, prefix=[3, 1, 2400, 0, 0, 64])])
+def test_prefill_few_rows_of_long_contexts(kw):
+    c = Case(131, [(2500, 3), (40, 5), (4100, 1), (0, 2), (1027, 30), (2047, 1)], **kw)
+    got = c.prefill()
+    ok()
+    c.check(got)
+    again = c.prefill()
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
 def test_prefill_block_scales_far_apart():
     # neighbouring blocks' V scales 2^70 apart, the weight on the small ones
     c = Case(12, [(200, 60)], spread=0, hq=4, hkv=2)
