@@ -74,9 +74,10 @@ __device__ __forceinline__ void zero_page_head(uint8_t* page, int first, int lan
   }
 }
 
-// softcap * tanh(x / softcap), all in log2 units: with E = 2^(2 x / softcap),
-// tanh = 1 - 2 / (E + 1). The subtraction loses at most 2^-23 of the cap, an
-// error of some 1e-5 in a score at the caps in use; a large E gives 2 / inf = 0.
+// softcap * tanh(x / softcap), all in log2 units, in two forms (inv = 1 / cap_log2).
+// With E = 2^(2 x / softcap), tanh = 1 - 2 / (E + 1): right to some 2^-23 of the cap,
+// which is little beside a score near the cap (a large E gives 2 / inf = 0) and much
+// beside a small one.
 __device__ __forceinline__ float softcap_log2(float x, float cap_log2, float two_over_cap) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * two_over_cap));
@@ -84,21 +85,47 @@ __device__ __forceinline__ float softcap_log2(float x, float cap_log2, float two
   return fmaf(-2.f * cap_log2, r, cap_log2);
 }
 
-// softcap_log2 of the N scores of a thread's row, of which it sees first..last; the
-// others (left-over bytes, maybe) become 0. Scores seldom leave (-softcap, softcap),
-// and there tanh(y) = y P(y^2) with P of degree 6 is off by less than 1.3e-7 (the
-// Chebyshev interpolant of tanh(sqrt t) / sqrt t on [0, 1], evaluated in fp32): five
-// packed operations a score, where the general form takes two of the special-function
-// unit's, which the softmax itself keeps busy. A row with a larger score takes that
-// one. The choice is the row's own, so that its bits depend neither on keys it does
-// not see nor on the warp's other rows (the warp choosing for all of its rows, unseen
-// keys included, took 103 us on the capped window where this takes 107).
+// Inside (-softcap, softcap), where scores seldom leave, tanh(y) = y P(y^2) with P of
+// degree 6 is off by less than 2e-7 of itself (the Chebyshev interpolant of
+// tanh(sqrt t) / sqrt t on [0, 1], evaluated in fp32): five packed operations a score,
+// where the other form takes two of the special-function unit's, which the softmax
+// keeps busy.
+__device__ __forceinline__ float2 softcap_log2_inside(float a, float b, float inv) {
+  constexpr float kP[7] = {0.99999994f, -0.33332857f, 0.13325398f, -0.053465176f,
+                           0.02030552f, -0.0062170699f, 0.0010455536f};
+  const f2 v = pack_f2(a, b);
+  const f2 y = mul2(v, pack_f2(inv, inv)), t = mul2(y, y);
+  f2 h = pack_f2(kP[6], kP[6]);
+#pragma unroll
+  for (int k = 5; k >= 0; --k) h = fma2(h, t, pack_f2(kP[k], kP[k]));
+  return unpack_f2(mul2(v, h));
+}
+
+// Two scores, each in its own form.
+__device__ __forceinline__ void softcap_log2_pair(float& a, float& b, float cap_log2,
+                                                  float two_over_cap) {
+  const float inv = two_over_cap * (0.5f * kLn2);
+  const float2 r = softcap_log2_inside(a, b, inv);
+  const bool in_a = fabsf(a) * inv <= 1.f, in_b = fabsf(b) * inv <= 1.f;
+  if (!(in_a && in_b)) {
+    a = in_a ? r.x : softcap_log2(a, cap_log2, two_over_cap);
+    b = in_b ? r.y : softcap_log2(b, cap_log2, two_over_cap);
+  } else {
+    a = r.x;
+    b = r.y;
+  }
+}
+
+// The N scores of a thread's row, of which it sees first..last; the others (left-over
+// bytes, maybe) become 0. The row takes one form for all of them: where one is beyond
+// the cap, 2^-23 of the cap is little beside the row's scores. The choice is the row's
+// own, so that its bits depend neither on keys it does not see nor on the warp's other
+// rows (the warp choosing for all of its rows, unseen keys included, took 103 us on
+// the capped window where this takes 107).
 template <int N>
 __device__ __forceinline__ void softcap_log2_row(float (&x)[N], int first, int last,
                                                  float cap_log2, float two_over_cap) {
-  constexpr float kP[7] = {0.99999994f, -0.33332857f, 0.13325398f, -0.053465176f,
-                           0.02030552f, -0.0062170699f, 0.0010455536f};
-  const float inv = two_over_cap * (0.5f * kLn2);       // 1 / cap_log2
+  const float inv = two_over_cap * (0.5f * kLn2);
   if (first > 0 || last < N - 1) {
     const unsigned span = (unsigned)(last - first);
 #pragma unroll
@@ -109,15 +136,9 @@ __device__ __forceinline__ void softcap_log2_row(float (&x)[N], int first, int l
 #pragma unroll
   for (int c = 0; c < N; ++c) top = fmaxf(top, fabsf(x[c]));
   if (top * inv <= 1.f) {
-    const f2 i2 = pack_f2(inv, inv);
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
-      const f2 v = pack_f2(x[c], x[c + 1]);
-      const f2 y = mul2(v, i2), t = mul2(y, y);
-      f2 h = pack_f2(kP[6], kP[6]);
-#pragma unroll
-      for (int k = 5; k >= 0; --k) h = fma2(h, t, pack_f2(kP[k], kP[k]));
-      const float2 r = unpack_f2(mul2(v, h));
+      const float2 r = softcap_log2_inside(x[c], x[c + 1], inv);
       x[c] = r.x;
       x[c + 1] = r.y;
     }

@@ -249,17 +249,33 @@ __global__ void __launch_bounds__(NW * 32)
     const bool v0 = tbase + tk0 < tok1 && tbase + tk0 >= first;
     const bool v8 = tbase + tk8 < tok1 && tbase + tk8 >= first;
     const float back0 = (float)(ctx - 1 - (tbase + tk0)), back8 = (float)(ctx - 1 - (tbase + tk8));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] *= ksl2;
+    // up to a cap of 128 the first form's error (3e-5 at most) is no more than the
+    // products behind a score have, and it is the faster one beside a page's other work
+    // (128 sequences of 1,024 to 8,192 keys 208 us; a choice per score 219)
+    if (ep.cap_log2 > 128.f / kLn2) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+          softcap_log2_pair(s[nt][e], s[nt][e + 1], ep.cap_log2, ep.two_over_cap);
+    } else if (ep.cap_log2 != 0.f) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[nt][e] = softcap_log2(s[nt][e], ep.cap_log2, ep.two_over_cap);
+    }
     float pmax[NT][2];
     bool move = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float x0 = s[nt][e] * ksl2, x8 = s[nt][2 + e] * ksl2;
-        if (ep.cap_log2 != 0.f) {
-          x0 = softcap_log2(x0, ep.cap_log2, ep.two_over_cap);
-          x8 = softcap_log2(x8, ep.cap_log2, ep.two_over_cap);
-        }
+        float x0 = s[nt][e], x8 = s[nt][2 + e];
         x0 = fmaf(-slope[nt][e], back0, x0);
         x8 = fmaf(-slope[nt][e], back8, x8);
         s[nt][e] = v0 ? x0 : -INFINITY;

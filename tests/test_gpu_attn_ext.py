@@ -434,6 +434,23 @@ def test_prefill_rows_do_not_depend_on_keys_they_do_not_see(kw):
         at += q
 
 
+@pytest.mark.parametrize("cap", [300.0, 1e6, 1e30, 2e38])
+@pytest.mark.parametrize("kw", [dict(), dict(kv="same", spread=1), dict(kv="head", d=64, dtype="f16"),
+                                dict(kv="same", spread=1, d=256)])
+def test_a_cap_far_above_the_scores(cap, kw):
+    # inside the cap tanh is right to 2e-7 of itself, so of the score: less than the 4 * 2^-23 of
+    # it that lse_tolerance and tolerance have for conversions. Nothing in the bound grows
+    # with the cap
+    c = Case(151, [(p + q - 1, 1) for p, q in CHUNKS], softcap=cap, **kw)
+    ref = c.want()
+    assert float(ref.size.max()) < 250                # sum |q k| * scale: no score reaches a cap
+    for out, lse in (c.decode(), c.prefill()):
+        ok()
+        err = (out.double() - ref.out).abs()
+        assert not (err > R.tolerance(ref, c.q.dtype, c.p_dtype)).any()
+        assert not ((lse.double() - ref.lse).abs() > R.lse_tolerance(ref)).any()
+
+
 def test_prefill_bad_sequences():
     c = Case(13, [(50, 10), (3, 20), (70, 8)])
     ref = c.want()
