@@ -26,7 +26,7 @@
 // sector), fetched while the pages are on their way.
 //
 // Bound: bytes (codes; 1/(BS D) of that for the scales). 128 sequences of 1,024 to
-// 8,192 keys, 32 / 8 heads, D = 128: 207 us, 6.2 TB/s, 0.92 of the measured copy
+// 8,192 keys, 32 / 8 heads, D = 128: 205 us, 6.3 TB/s, 0.93 of the measured copy
 // rate; a window of 1,024 at D = 256, bf16, 32 sequences: 45 us, 5.8 TB/s. Few and
 // short contexts are bound by the chain of a CTA (length, table, pages, merge): one
 // sequence of 700 keys 7.3 us.
