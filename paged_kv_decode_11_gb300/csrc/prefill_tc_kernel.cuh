@@ -354,7 +354,9 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   const bool v_warp = warp >= Cfg::W_V && warp < Cfg::W_V + Cfg::PV;
   const bool producer = k_warp || v_warp;
   const int np = k_warp ? Cfg::PK : Cfg::PV;              // producers of this operand
-  const int pw = k_warp ? warp - Cfg::W_K : warp - Cfg::W_V;   // boxes pw, pw + np, ..
+  const int pw = Cfg::PK == 1 && Cfg::PV == 1 ? 0           // boxes pw, pw + np, ..
+                 : k_warp                     ? warp - Cfg::W_K
+                                              : warp - Cfg::W_V;
   const CUtensorMap* tmap = k_warp ? &tmK : &tmV;
   uint64_t* full_x = k_warp ? full_k : full_v;
   uint64_t* empty_x = k_warp ? empty_k : empty_v;
