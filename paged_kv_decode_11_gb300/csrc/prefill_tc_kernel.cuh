@@ -1174,7 +1174,11 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
     ao[o] = theirs[o].x == -INFINITY ? 0.f : ex2_approx(theirs[o].x - M2);
     L2 += theirs[o].y * ao[o];
   }
-  float inv = L2 > 0.f ? (KV8 && !BSC ? p.v_scales[h] : 1.f) / L2 : 0.f;
+  // MODE: a NaN sum is no empty row. A group or CTA for whose keys a row has nothing but
+  // NaN keeps no reference, so its O has weight 0 above, but its sum is NaN and makes
+  // the row so
+  const bool some = MODE == kTcPlain ? L2 > 0.f : !(L2 == 0.f);
+  float inv = some ? (KV8 && !BSC ? p.v_scales[h] : 1.f) / L2 : 0.f;
   if constexpr (BSC) {
     // O 2^W against its sum L2 2^M2
     float W2 = W;
@@ -1221,7 +1225,7 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
     }
   }
   if (split == 0 && grp == 0 && rvalid && p.out_lse != nullptr)
-    p.out_lse[(int64_t)(q0 + qi) * p.Hq + hq] = L2 > 0.f ? (M2 + log2f(L2)) * kLn2 : -INFINITY;
+    p.out_lse[(int64_t)(q0 + qi) * p.Hq + hq] = some ? (M2 + log2f(L2)) * kLn2 : -INFINITY;
   tc::fence_before();
   named_barrier(1, NG * kTcRows);
   if (warp == 0) tc::dealloc(tm, Cfg::TMEM_COLS);

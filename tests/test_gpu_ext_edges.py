@@ -1,0 +1,85 @@
+"""paged_attn_decode_ext, paged_attn_prefill_chunk_ext and the step that composes them where a
+row's keys are NaN, where calls of other sizes share a workspace, and at bounds of the arguments."""
+import pytest
+import torch
+
+import paged_kv_decode_11_gb300 as P
+from tests import ext_ref as R
+from tests.test_gpu_attn_ext import Case, ok
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from paged_kv_decode_11_gb300 import build
+    build.build()
+    P.load()
+    torch.cuda.init()
+    P.pkv_get_device_error()
+
+
+def nan_blocks(c, n, first, which, head=1):
+    """NaN scales for one KV head on the blocks of sequence n from number `first` on."""
+    blocks = c.tables[n][c.tables[n] >= 0][first:].long()
+    getattr(c, which)[blocks, head] = 255
+
+
+# (cached, new tokens) and the first position whose blocks are NaN: a row that sees nothing
+# else (the only block; the whole context), the page behind a border between key tiles (of 128
+# keys, 64 at head_dim 256), the last tiles of a long context whose tiles a cluster's CTAs share
+NAN_PLACES = [([(0, 20)], 0), ([(5, 11)], 0), ([(0, 130)], 128), ([(127, 3)], 128), ([(60, 6)], 64),
+              ([(0, 400)], 384), ([(4090, 7)], 0), ([(4090, 7)], 3840), ([(4090, 7)], 2048),
+              ([(4090, 7)], 4096)]
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=9.0, alibi=True), dict(d=64), dict(d=256),
+                                dict(dtype="f16", bs=64)])
+@pytest.mark.parametrize("which", ["ks", "vs"])
+@pytest.mark.parametrize("seqs,at", NAN_PLACES)
+def test_prefill_nan_scales_are_all_a_share_sees(seqs, at, which, kw):
+    # as many copies of the sequence as make clusters of eight, four, two and one CTA per tile
+    for copies in (1, 12, 24, 60) if sum(seqs[0]) > 4000 else (1,):
+        c = Case(200, seqs * copies, **kw)
+        ref = c.want()
+        p, q = seqs[0]
+        bs = c.k.shape[2]
+        for n in {0, copies - 1}:
+            nan_blocks(c, n, at // bs, which)
+        out, lse = c.prefill()
+        ok()
+        sees = torch.arange(p, p + q).cuda() >= at // bs * bs
+        tol = R.tolerance(ref, c.q.dtype, c.p_dtype, c.softcap)
+        near = (out.double() - ref.out).abs() <= tol
+        lse_near = (lse.double() - ref.lse).abs() <= R.lse_tolerance(ref, c.softcap)
+        for n in range(copies):
+            rows = slice(n * q, (n + 1) * q)
+            bad = torch.zeros(q, c.q.shape[1], dtype=torch.bool, device="cuda")
+            if n in (0, copies - 1):
+                bad[sees, 4:] = True
+            assert out[rows][bad].isnan().all()
+            assert near[rows][~bad].all() and lse_near[rows][~bad].all()
+            if which == "ks":
+                assert lse[rows][bad].isnan().all()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(dtype="f16", softcap=9.0), dict(d=64, alibi=True), dict(d=256),
+    dict(kv="head", softcap=9.0), dict(kv="head", d=256, dtype="f16", window=20),
+    dict(kv="same", spread=1, softcap=9.0), dict(kv="same", spread=1, alibi=True, dtype="f16", d=64),
+    dict(kv="same", spread=1, d=256), dict(kv="same", spread=1, window=30, prefix=[3, 700, 0])])
+def test_prefill_nan_query_rows_stay_nan(kw):
+    c = Case(201, [(10, 5), (0, 300), (3000, 4)], **kw)
+    ref = c.want()
+    at = [(2, 0), (7, 5), (100, 3), (304, 7), (306, 4)]
+    for row, head in at:
+        c.q[row, head, row % 64] = float("nan")
+    out, lse = c.prefill()
+    ok()
+    bad = torch.zeros(c.q.shape[:2], dtype=torch.bool, device="cuda")
+    for row, head in at:
+        bad[row, head] = True
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    tol = R.tolerance(ref, c.q.dtype, c.p_dtype, c.softcap)
+    assert ((out.double() - ref.out).abs() <= tol)[~bad].all()
+    assert ((lse.double() - ref.lse).abs() <= R.lse_tolerance(ref, c.softcap))[~bad].all()
