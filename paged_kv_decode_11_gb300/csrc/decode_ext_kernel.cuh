@@ -404,11 +404,12 @@ __global__ void __launch_bounds__(NW * 32)
     float L = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (red_m[w][hh] != -INFINITY) L += red_l[w][hh] * exp2f(red_m[w][hh] - M);
+      // (a warp with no reference has a sum of 0, or NaN where NaN is all it saw)
+      L += red_m[w][hh] == -INFINITY ? red_l[w][hh] : red_l[w][hh] * exp2f(red_m[w][hh] - M);
       o0 += obuf[(w * G + hh) * D + d];
       o1 += obuf[(w * G + hh) * D + d + 1];
     }
-    const bool nonempty = L > 0.f;
+    const bool nonempty = !(L == 0.f);               // (a NaN sum is no empty row)
     float inv = nonempty ? 1.f / L : 0.f;
     if constexpr (BSC) {
       // out = (sum of weights times codes) 2^(their reference) / (L 2^M)

@@ -21,7 +21,8 @@ def _lib():
 
 def nan_blocks(c, n, first, which, head=1):
     """NaN scales for one KV head on the blocks of sequence n from number `first` on."""
-    blocks = c.tables[n][c.tables[n] >= 0][first:].long()
+    ids = c.tables[n].tolist()                  # (blocks before a window have no entry)
+    blocks = [b for b in ids if 0 <= b < c.k.shape[0]][first:]
     getattr(c, which)[blocks, head] = 255
 
 
@@ -79,6 +80,50 @@ def test_prefill_nan_query_rows_stay_nan(kw):
     bad = torch.zeros(c.q.shape[:2], dtype=torch.bool, device="cuda")
     for row, head in at:
         bad[row, head] = True
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    tol = R.tolerance(ref, c.q.dtype, c.p_dtype, c.softcap)
+    assert ((out.double() - ref.out).abs() <= tol)[~bad].all()
+    assert ((lse.double() - ref.lse).abs() <= R.lse_tolerance(ref, c.softcap))[~bad].all()
+
+
+@pytest.mark.parametrize("part", [0, 16, 512])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=9.0, alibi=True), dict(d=64, window=900),
+                                dict(d=256, bs=32), dict(softcap=300.0)])
+@pytest.mark.parametrize("which", ["ks", "vs"])
+def test_decode_nan_scales_and_their_lse(which, kw, part):
+    # the NaN blocks: the whole context, the last page alone (one warp's, or one partition's), the
+    # later half. A NaN K scale makes scores NaN, so out and lse; a NaN V scale out alone
+    lens, first = [5, 16, 33, 700, 2500, 2500, 2500], [0, 0, 32, 688, 0, 2496, 1300]
+    c = Case(202, [(n - 1, 1) for n in lens + [300]], **kw)
+    ref = c.want()
+    for n, at in enumerate(first):
+        nan_blocks(c, n, 0 if c.window else at // c.k.shape[2], which)
+    out, lse = c.decode(part)
+    ok()
+    bad = torch.zeros(c.q.shape[:2], dtype=torch.bool, device="cuda")
+    bad[:len(lens), 4:] = True
+    assert out[bad].isnan().all()
+    tol = R.tolerance(ref, c.q.dtype, c.p_dtype, c.softcap)
+    assert ((out.double() - ref.out).abs() <= tol)[~bad].all()
+    near = (lse.double() - ref.lse).abs() <= R.lse_tolerance(ref, c.softcap)
+    assert near[~bad].all()
+    assert lse[bad].isnan().all() if which == "ks" else near.all()
+
+
+@pytest.mark.parametrize("part", [0, 16])
+@pytest.mark.parametrize("kw", [
+    dict(dtype="f16", softcap=9.0), dict(kv="head", d=256, dtype="f16", window=20),
+    dict(kv="same", spread=1, softcap=9.0), dict(kv="same", spread=1, alibi=True, dtype="f16", d=64),
+    dict(kv="same", spread=1, d=256), dict(hq=2), dict(kv="head", hq=2, softcap=400.0)])
+def test_decode_nan_query_rows_stay_nan(kw, part):
+    # (over an E4M3 cache a KV head's bf16 queries share a power of two: one of a group alone)
+    c = Case(203, [(n - 1, 1) for n in (1, 40, 700, 3000)], **kw)
+    ref = c.want()
+    bad = torch.zeros(c.q.shape[:2], dtype=torch.bool, device="cuda")
+    bad[0, 0] = bad[2, 1] = bad[3, c.q.shape[1] - 1] = True
+    c.q[..., 3].masked_fill_(bad, float("nan"))
+    out, lse = c.decode(part)
+    ok()
     assert out[bad].isnan().all() and lse[bad].isnan().all()
     tol = R.tolerance(ref, c.q.dtype, c.p_dtype, c.softcap)
     assert ((out.double() - ref.out).abs() <= tol)[~bad].all()
