@@ -351,7 +351,10 @@ __global__ void __launch_bounds__(NW * 32)
     for (int e = 0; e < 2; ++e) {
       l[nt][e] = col_sum8(l[nt][e]);
       if (g == 0) {
-        red_m[warp][8 * nt + 2 * c + e] = m[nt][e];
+        // (a warp that saw nothing but NaN scores has no reference, but its sum is NaN: any
+        // finite reference takes that to the merged sum)
+        red_m[warp][8 * nt + 2 * c + e] =
+            l[nt][e] != l[nt][e] ? fmaxf(m[nt][e], -3e38f) : m[nt][e];
         red_l[warp][8 * nt + 2 * c + e] = l[nt][e];
         if constexpr (BSC) red_w[warp][8 * nt + 2 * c + e] = mw[nt][e];
       }
@@ -404,8 +407,7 @@ __global__ void __launch_bounds__(NW * 32)
     float L = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      // (a warp with no reference has a sum of 0, or NaN where NaN is all it saw)
-      L += red_m[w][hh] == -INFINITY ? red_l[w][hh] : red_l[w][hh] * exp2f(red_m[w][hh] - M);
+      if (red_m[w][hh] != -INFINITY) L += red_l[w][hh] * exp2f(red_m[w][hh] - M);
       o0 += obuf[(w * G + hh) * D + d];
       o1 += obuf[(w * G + hh) * D + d + 1];
     }
