@@ -738,10 +738,18 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   };
   uint32_t sc_cur = scales_of(0), sc_next = scales_of(1);
   int sc_chunk = 0;
+  // which of the warp's 32 pages have a NaN scale
+  auto nan_scales = [](uint32_t sc) {
+    return __ballot_sync(0xffffffffu, (sc & 0xFFu) == 255u || sc >> 8 == 255u);
+  };
+  uint32_t sc_nan = BSC ? nan_scales(sc_cur) : 0u;
   const uint32_t tOg = tO + grp * D;
   const int n_mine = (n_tiles - grp + NG - 1) / NG;     // this group's tiles
   // the references of the probabilities and their sum, and (BSC) of P and O
   float m_ref = -INFINITY, w_ref = -INFINITY, l = 0.f;
+  // BSC: NaN once the row sees a page whose K scale (what is added to l) or V scale (to
+  // O's factor) is, else 0
+  float k_nan = 0.f, v_nan = 0.f;
 
   for (int j = 0; j < n_mine; ++j) {
     const int u = NG * j + grp;                         // local tile
@@ -857,12 +865,21 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
       // on its way from tensor memory meanwhile, 326; CH = 16 319).
       constexpr int CH = 32, NCH = kTcKeys / CH, PPC = CH / kBS;
       float x[CH], kf[PPC], ev[PPC];
-      float nan_or_0[PPC];                                // BSC: NaN where a scale of the page is
-      bool nan_scale = false;
       if constexpr (BSC) {
         if ((u * kTcPages) / 32 != sc_chunk) {
           sc_cur = sc_next;
           sc_next = scales_of(++sc_chunk + 1);
+          sc_nan = nan_scales(sc_cur);
+        }
+        const int p0 = (u * kTcPages) % 32;
+        for (uint32_t nans = (sc_nan >> p0) & ((1u << kTcPages) - 1u); nans != 0u; nans &= nans - 1u) {
+          const int pg = __ffs(nans) - 1, key0 = t * kTcKeys + kBS * pg;
+          const uint32_t sc = __shfl_sync(0xffffffffu, sc_cur, p0 + pg);
+          if (key0 <= last && key0 + kBS > lo) {
+            const float nan = __int_as_float(0x7FFFFFFF);
+            if ((sc & 0xFFu) == 255u) k_nan = nan;
+            if (sc >> 8 == 255u) v_nan = nan;
+          }
         }
       }
       auto load = [&](int i) {
@@ -873,9 +890,6 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
           for (int pg = 0; pg < PPC; ++pg) {
             const uint32_t sc =
                 __shfl_sync(0xffffffffu, sc_cur, (u * kTcPages + PPC * i + pg) % 32);
-            const bool bad = (sc & 0xFFu) == 255u || sc >> 8 == 255u;
-            nan_scale = (pg > 0 && nan_scale) || bad;
-            nan_or_0[pg] = bad ? __int_as_float(0x7FFFFFFF) : 0.f;
             // (not below the least normal number, so that a masked -inf stays -inf)
             kf[pg] = fmaxf(sl2 * pow2_any(min((int)(sc & 0xFFu), 254) - kE8M0Bias), 0x1p-126f);
             ev[pg] = (float)((int)(sc >> 8) - kE8M0Bias);
@@ -886,16 +900,12 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
         for (int c = 0; c < CH; ++c) x[c] = __uint_as_float(v[c]);
       };
       // Keys the row does not see become -inf (only in chunks that cross a limit).
-      // BSC: keys of a page whose scale is NaN become NaN for the rows that see them
-      // (and only for those: a masked score times a NaN factor would be one too).
       auto mask = [&](int k0) {
-        if (k0 + CH - 1 > last || (MOD && k0 < lo) || (BSC && nan_scale)) {
+        if (k0 + CH - 1 > last || (MOD && k0 < lo)) {
           const unsigned span = (unsigned)(last - lo);
 #pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            if constexpr (BSC) x[c] += nan_or_0[c / kBS];
+          for (int c = 0; c < CH; ++c)
             if ((unsigned)(k0 - lo + c) > span) x[c] = -INFINITY;
-          }
         }
       };
       float mx = -INFINITY, mxw = -INFINITY;              // largest score, largest score + ev
@@ -1059,22 +1069,28 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
     wait(&done_bar, 0);
     tc::fence_after();
   }
-  // (BSC: the reference of O apart from that of the sum)
+  // (BSC: the reference of O apart from that of the sum, and the NaN of a V scale)
   using Share = std::conditional_t<BSC, float4, float2>;
   Share* ml_g0 = Cfg::PTM ? reinterpret_cast<Share*>(pQ) : reinterpret_cast<Share*>(pP);
   Share* ml_g1 = Cfg::PTM ? reinterpret_cast<Share*>(pQ) + kTcRows
                           : reinterpret_cast<Share*>(pP + NSB * Cfg::P_BYTES);
   Share mine;
   mine.x = m_ref;
-  mine.y = l;
-  if constexpr (BSC) mine.z = w_ref;
+  mine.y = BSC ? l + k_nan : l;
+  if constexpr (BSC) {
+    mine.z = w_ref;
+    mine.w = v_nan;
+  }
   (grp == 0 ? ml_g0 : ml_g1)[r] = mine;
   named_barrier(1, NG * kTcRows);
   const Share ml0 = ml_g0[r];
   Share ml1;
   ml1.x = -INFINITY;
   ml1.y = 0.f;
-  if constexpr (BSC) ml1.z = -INFINITY;
+  if constexpr (BSC) {
+    ml1.z = -INFINITY;
+    ml1.w = 0.f;
+  }
   if constexpr (NG > 1) ml1 = ml_g1[r];
   // a group with no tile has no O
   const bool has0 = n_tiles > 0, has1 = NG > 1 && n_tiles > 1;
@@ -1082,8 +1098,9 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   float f0 = has0 && ml0.x != -INFINITY ? ex2_approx(ml0.x - M) : 0.f;
   float f1 = has1 && ml1.x != -INFINITY ? ex2_approx(ml1.x - M) : 0.f;
   const float Lc = ml0.y * f0 + ml1.y * f1;
-  float W = M;                                          // the reference of O
+  float W = M, vn = 0.f;                                // the reference of O
   if constexpr (BSC) {
+    vn = ml0.w + ml1.w;
     W = fmaxf(ml0.z, ml1.z);
     f0 = has0 && ml0.z != -INFINITY ? ex2_approx(ml0.z - W) : 0.f;
     f1 = has1 && ml1.z != -INFINITY ? ex2_approx(ml1.z - W) : 0.f;
@@ -1124,7 +1141,10 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   for (int o = 0; o < NO; ++o) {
     theirs[o].x = -INFINITY;
     theirs[o].y = 0.f;
-    if constexpr (BSC) theirs[o].z = -INFINITY;
+    if constexpr (BSC) {
+      theirs[o].z = -INFINITY;
+      theirs[o].w = 0.f;
+    }
   }
   const uint32_t recv_rows = sKV;
   const uint32_t recv_ml = sKV + NO * O_BYTES;
@@ -1152,7 +1172,7 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
       }
       if (grp == 0) {
         const uint32_t at = cluster_map(recv_ml + (place * kTcRows + r) * sizeof(Share), other);
-        if constexpr (BSC) st_cluster_v4(at, M, Lc, W, 0.f);
+        if constexpr (BSC) st_cluster_v4(at, M, Lc, W, vn);
         else st_cluster_v2(at, M, Lc);
       }
       mbar_arrive_remote(cluster_map(smem_u32(&recv_bar), other));
@@ -1188,7 +1208,9 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
 #pragma unroll
     for (int o = 0; o < NO; ++o)
       ao[o] = theirs[o].z == -INFINITY ? 0.f : ex2_approx(theirs[o].z - W2);
-    inv *= W2 == -INFINITY ? 0.f : exp2f(W2 - M2);
+    inv = fmaf(inv, W2 == -INFINITY ? 0.f : exp2f(W2 - M2), vn);
+#pragma unroll
+    for (int o = 0; o < NO; ++o) inv += theirs[o].w;
   }
   const float4* orecv = reinterpret_cast<const float4*>(basep + (recv_rows - base)) + r;
   uint16_t* orow = static_cast<uint16_t*>(p.out) + ((int64_t)(q0 + (rvalid ? qi : 0)) * p.Hq +

@@ -64,6 +64,22 @@ def test_prefill_nan_scales_are_all_a_share_sees(seqs, at, which, kw):
                 assert lse[rows][bad].isnan().all()
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=9.0, alibi=True), dict(d=64), dict(d=256),
+                                dict(dtype="f16", window=600)])
+@pytest.mark.parametrize("seqs,at", NAN_PLACES)
+def test_prefill_nan_v_scales_leave_lse_alone(seqs, at, kw):
+    # lse is a sum over scores, in which V has no part
+    for copies in (1, 12, 24, 60) if sum(seqs[0]) > 4000 else (1,):
+        c = Case(204, seqs * copies, **kw)
+        ref = c.want()
+        for n in {0, copies - 1}:
+            nan_blocks(c, n, 0 if c.window else at // c.k.shape[2], "vs")
+        out, lse = c.prefill()
+        ok()
+        assert out[0 if c.window else -1, 4:].isnan().all()
+        assert ((lse.double() - ref.lse).abs() <= R.lse_tolerance(ref, c.softcap)).all()
+
+
 @pytest.mark.parametrize("kw", [
     dict(), dict(dtype="f16", softcap=9.0), dict(d=64, alibi=True), dict(d=256),
     dict(kv="head", softcap=9.0), dict(kv="head", d=256, dtype="f16", window=20),
