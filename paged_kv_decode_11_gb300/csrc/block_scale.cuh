@@ -74,6 +74,10 @@ __device__ __forceinline__ void zero_page_head(uint8_t* page, int first, int lan
   }
 }
 
+// Up to this cap the error of the first form below, 3e-5 at most, is no more than the
+// products behind a score have.
+constexpr float kCoarseCap = 128.f;
+
 // softcap * tanh(x / softcap), all in log2 units, in two forms (inv = 1 / cap_log2).
 // With E = 2^(2 x / softcap), tanh = 1 - 2 / (E + 1): right to some 2^-23 of the cap,
 // which is little beside a score near the cap (a large E gives 2 / inf = 0) and much
@@ -116,12 +120,26 @@ __device__ __forceinline__ void softcap_log2_pair(float& a, float& b, float cap_
   }
 }
 
+// N scores, each in its own form. Out of line and in local memory: beside the loop that
+// calls it, code that hardly ever runs costs what it displaces (inline 111.6 us on the
+// capped window, so 107.8, without it 106.8).
+template <int N>
+__device__ __noinline__ void softcap_log2_each(float* x, float cap_log2, float two_over_cap) {
+  for (int c = 0; c < N; c += 2) {
+    float a = x[c], b = x[c + 1];
+    softcap_log2_pair(a, b, cap_log2, two_over_cap);
+    x[c] = a;
+    x[c + 1] = b;
+  }
+}
+
 // The N scores of a thread's row, of which it sees first..last; the others (left-over
-// bytes, maybe) become 0. The row takes one form for all of them: where one is beyond
-// the cap, 2^-23 of the cap is little beside the row's scores. The choice is the row's
-// own, so that its bits depend neither on keys it does not see nor on the warp's other
-// rows (the warp choosing for all of its rows, unseen keys included, took 103 us on
-// the capped window where this takes 107).
+// bytes, maybe) become 0. The row takes one form for all of them, the first where one is
+// beyond a cap of up to kCoarseCap. Beyond a larger cap each takes its own: a score below
+// -cap weighs nothing, and the others may be small beside 2^-23 of the cap. The choice is
+// the row's own, so that its bits depend neither on keys it does not see nor on the
+// warp's other rows (the warp choosing for all of its rows, unseen keys included, took
+// 103 us on the capped window where a choice by row takes 107).
 template <int N>
 __device__ __forceinline__ void softcap_log2_row(float (&x)[N], int first, int last,
                                                  float cap_log2, float two_over_cap) {
@@ -132,10 +150,10 @@ __device__ __forceinline__ void softcap_log2_row(float (&x)[N], int first, int l
     for (int c = 0; c < N; ++c)
       if ((unsigned)(c - first) > span) x[c] = 0.f;
   }
-  float top = 0.f;
+  float far = 0.f;
 #pragma unroll
-  for (int c = 0; c < N; ++c) top = fmaxf(top, fabsf(x[c]));
-  if (top * inv <= 1.f) {
+  for (int c = 0; c < N; ++c) far = fmaxf(far, fabsf(x[c]));
+  if (far * inv <= 1.f) {
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
       const float2 r = softcap_log2_inside(x[c], x[c + 1], inv);
@@ -143,6 +161,15 @@ __device__ __forceinline__ void softcap_log2_row(float (&x)[N], int first, int l
       x[c + 1] = r.y;
     }
   } else {
+    if (__builtin_expect(cap_log2 > kCoarseCap / kLn2, 0)) {
+      float t[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) t[c] = x[c];
+      softcap_log2_each<N>(t, cap_log2, two_over_cap);
+#pragma unroll
+      for (int c = 0; c < N; ++c) x[c] = t[c];
+      return;
+    }
 #pragma unroll
     for (int c = 0; c < N; ++c) x[c] = softcap_log2(x[c], cap_log2, two_over_cap);
   }

@@ -253,10 +253,9 @@ __global__ void __launch_bounds__(NW * 32)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[nt][e] *= ksl2;
-    // up to a cap of 128 the first form's error (3e-5 at most) is no more than the
-    // products behind a score have, and it is the faster one beside a page's other work
-    // (128 sequences of 1,024 to 8,192 keys 208 us; a choice per score 219)
-    if (ep.cap_log2 > 128.f / kLn2) {
+    // up to kCoarseCap the first form is good enough, and it is the faster one beside a
+    // page's other work (128 sequences of 1,024 to 8,192 keys 208 us; a choice per score 219)
+    if (ep.cap_log2 > kCoarseCap / kLn2) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

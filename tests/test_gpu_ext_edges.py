@@ -144,3 +144,36 @@ def test_decode_nan_query_rows_stay_nan(kw, part):
     tol = R.tolerance(ref, c.q.dtype, c.p_dtype, c.softcap)
     assert ((out.double() - ref.out).abs() <= tol)[~bad].all()
     assert ((lse.double() - ref.lse).abs() <= R.lse_tolerance(ref, c.softcap))[~bad].all()
+
+
+@pytest.mark.parametrize("cap", [300.0, 1e4, 1e6, 1e30])
+@pytest.mark.parametrize("kw", [dict(kv="same", spread=1), dict(kv="same", spread=1, d=256),
+                                dict(kv="same", spread=1, d=64, window=90), dict()])
+def test_a_score_below_minus_the_cap_leaves_the_others_alone(cap, kw):
+    # Keys whose scores lie far below -cap weigh nothing (e^-cap at most), so the bound is that of
+    # the other keys: nothing in it grows with the cap, or with those scores
+    seqs = [(40, 60), (0, 100), (300, 1)]
+    c = Case(205, seqs, softcap=cap, **kw)
+    c.q[..., 0] = 8.0
+    c.k[..., 0] = 0
+    size = c.want().size
+    big = 2.0 ** torch.tensor(3 * cap / (8 * c.scale)).log2().ceil().item()   # a score of -3 cap or below
+    bs = c.k.shape[2]
+    for n, (p, q) in enumerate(seqs):
+        j = max(0, p + q - 30) // bs * bs                   # within every row's window, if it sees it
+        block = int(c.tables[n, j // bs])
+        if c.ks is not None:
+            c.k[block] = 0
+            c.k[block, ..., 0] = -1
+            c.ks[block] = 127 + int(torch.tensor(big).log2().item())
+        else:
+            c.k[block, :, 3, 0] = -big
+    ref = c.want()
+    # rows that see nothing else (the first of an empty context may) are no test of this
+    rows = ref.lse.min(1).values > -cap / 2
+    assert rows.sum() > 100
+    ref.size = size
+    for out, lse in (c.prefill(),):
+        ok()
+        assert ((out.double() - ref.out).abs() <= R.tolerance(ref, c.q.dtype, c.p_dtype))[rows].all()
+        assert ((lse.double() - ref.lse).abs() <= R.lse_tolerance(ref))[rows].all()
