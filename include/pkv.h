@@ -445,7 +445,12 @@ pkv_status rope_append_block_scaled(const void* key, const void* value, pkv_dtyp
 /*
  * paged_attn_decode_ext_workspace_size — bytes of workspace that
  *   paged_attn_decode_ext needs (window as passed to it); 0 for invalid sizes.
- *   The rules of paged_attn_decode_workspace_size apply.
+ *   Query on the device that will run the call. Zero-fill the workspace once
+ *   before its first use, and again after a call that ended with a device
+ *   error; apart from that calls of paged_attn_decode_ext of any sizes may use
+ *   it in turn, captured in graphs or not. (The other entry points with a
+ *   workspace expect their counters at zero, which calls of other sizes
+ *   overwrite: give them one of their own.)
  */
 size_t paged_attn_decode_ext_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
                                             int head_dim, int max_seq_len, int window,
@@ -467,8 +472,9 @@ size_t paged_attn_decode_ext_workspace_size(int num_seqs, int num_q_heads, int n
  *   read, and their block table entries may hold anything.
  *   scale is positive and finite, softcap finite. seq_lens[b] == 0 gives
  *   out = 0, lse = -inf. BS 16, 32 or 64; everything else as
- *   paged_attn_decode (workspace rules, partition_tokens, errors, programmatic
- *   launch).
+ *   paged_attn_decode (a workspace of paged_attn_decode_ext_workspace_size()
+ *   bytes, partition_tokens, errors, programmatic launch), but for contexts cut
+ *   into more than 2^23 partitions, which are PKV_ERR_UNSUPPORTED.
  */
 pkv_status paged_attn_decode_ext(void* out, const void* q, pkv_dtype q_dtype,
                                  const void* k_cache, const void* v_cache, pkv_dtype kv_dtype,

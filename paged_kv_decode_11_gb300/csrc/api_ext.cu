@@ -106,6 +106,7 @@ pkv_status paged_attn_decode_ext(void* out, const void* q, pkv_dtype q_dtype, co
   const pkv_dtype page_dtype = block_scaled ? PKV_FP8_E4M3 : kv_dtype;
   const DecodePlan pl = plan_decode_ext(num_seqs, num_q_heads, num_kv_heads, head_dim, span,
                                         partition_tokens, page_dtype == PKV_FP8_E4M3, sms);
+  if (pl.max_parts > kMaxDecodeExtParts) return PKV_ERR_UNSUPPORTED;
   if (workspace == nullptr || workspace_bytes < pl.bytes ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PKV_ERR_WORKSPACE;

@@ -38,6 +38,36 @@
 
 namespace pkv {
 
+// Partial results are stored without subnormals (see count_partition).
+__device__ __forceinline__ float mul_ftz(float a, float b) {
+  float r;
+  asm("mul.rn.ftz.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Counts a finished partition of a (sequence, KV head) and returns how many were counted
+// before it, out of nparts (at most kMaxDecodeExtParts). The counter is 0 between calls of
+// one size, but calls of other sizes that the workspace served may have put partial
+// results there. Two of those floats make no number below nparts but 0, as none is
+// subnormal: the first CTA to find such a word starts the count in its place, and those
+// that added to it meanwhile add again. A word can change under a CTA at most twice for
+// each of the other partitions.
+__device__ __forceinline__ unsigned int count_partition(unsigned long long* ctr, int nparts,
+                                                        unsigned int* err) {
+  unsigned long long before = atom_add_acq_rel_gpu(ctr, 1ull);
+  for (int i = 0; before >= (unsigned long long)nparts; ++i) {
+    if (i > 3 * nparts) {                          // another call is counting here too
+      atomicOr(err, PKV_DEVERR_COUNTER);
+      return 0u;
+    }
+    unsigned long long now;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(now) : "l"(ctr) : "memory");
+    if (now < (unsigned long long)nparts) before = atom_add_acq_rel_gpu(ctr, 1ull);
+    else if (atom_cas_acq_rel_gpu(ctr, now, 1ull) == now) return 0u;
+  }
+  return (unsigned int)before;
+}
+
 template <int D, int KV, int NT, int NW, int NST>
 struct DecodeExtCfg {
   using Geo = PageGeom<D, KV>;
@@ -365,7 +395,7 @@ __global__ void __launch_bounds__(NW * 32)
     // (b, h) counter still completes and comes back to zero
     if (nparts > 1 && tid == 0) {
       unsigned long long* ctr = p.done + (int64_t)b * p.Hkv + h;
-      if (atom_add_acq_rel_gpu(ctr, 1ull) + 1 == (unsigned long long)nparts) *ctr = 0ull;
+      if ((int)count_partition(ctr, nparts, p.err) + 1 == nparts) *ctr = 0ull;
     }
     return;
   }
@@ -424,21 +454,17 @@ __global__ void __launch_bounds__(NW * 32)
         p.out_lse[row0 + hh] = nonempty ? (M + log2f(L)) * kLn2 : -INFINITY;
     } else {
       const int64_t wrow = (row0 + hh) * p.max_parts + part_idx;
-      *reinterpret_cast<float2*>(p.ws_o + wrow * D + d) = make_float2(o0 * inv, o1 * inv);
-      if (d == 0) p.ws_lse[wrow] = nonempty ? M + log2f(L) : -INFINITY;
+      *reinterpret_cast<float2*>(p.ws_o + wrow * D + d) = make_float2(mul_ftz(o0, inv), mul_ftz(o1, inv));
+      if (d == 0) p.ws_lse[wrow] = nonempty ? mul_ftz(M + log2f(L), 1.f) : -INFINITY;
     }
   }
   if (nparts == 1) return;
 
   // ---- the CTA that completes the last partition of (b, h) merges them ------------------
-  // (counters and bulk-copied partials as in decode_kernel.cuh)
+  // (bulk-copied partials as in decode_kernel.cuh)
   __syncthreads();
   unsigned long long* ctr = p.done + (int64_t)b * p.Hkv + h;
-  if (tid == 0) {
-    const unsigned long long before = atom_add_acq_rel_gpu(ctr, 1ull);
-    if (before >= (unsigned long long)nparts) atomicOr(p.err, PKV_DEVERR_COUNTER);
-    s_last = (before + 1 == (unsigned long long)nparts);
-  }
+  if (tid == 0) s_last = (int)count_partition(ctr, nparts, p.err) + 1 == nparts;
   __syncthreads();
   if (!s_last) return;
   if (tid == 0) *ctr = 0ull;

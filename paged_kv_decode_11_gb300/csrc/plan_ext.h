@@ -8,6 +8,10 @@
 
 namespace pkv {
 
+// Partitions of a context: a count of them is told from two floats by being smaller
+// than the bits of any normal one.
+constexpr int kMaxDecodeExtParts = 1 << 23;
+
 // CTAs of kDecodeWarps warps an SM holds: the rings (3 stages of E4M3 pages or 2
 // of 16-bit ones per warp, K and V) are what bounds them, 8 at most.
 inline int decode_ext_ctas_per_sm(int head_dim, bool e4m3) {

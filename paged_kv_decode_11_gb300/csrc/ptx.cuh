@@ -286,6 +286,16 @@ __device__ __forceinline__ unsigned long long atom_add_acq_rel_gpu(unsigned long
                : "memory");
   return old;
 }
+__device__ __forceinline__ unsigned long long atom_cas_acq_rel_gpu(unsigned long long* p,
+                                                                   unsigned long long expected,
+                                                                   unsigned long long v) {
+  unsigned long long old;
+  asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
+               : "=l"(old)
+               : "l"(p), "l"(expected), "l"(v)
+               : "memory");
+  return old;
+}
 
 }  // namespace pkv
 

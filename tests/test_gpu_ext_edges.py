@@ -177,3 +177,53 @@ def test_a_score_below_minus_the_cap_leaves_the_others_alone(cap, kw):
         ok()
         assert ((out.double() - ref.out).abs() <= R.tolerance(ref, c.q.dtype, c.p_dtype))[rows].all()
         assert ((lse.double() - ref.lse).abs() <= R.lse_tolerance(ref))[rows].all()
+
+
+def test_calls_of_other_sizes_share_a_workspace_in_turn():
+    # a buffer made for the largest call serves all of them, whichever ran before: the
+    # partial results of one lie where another has its counters
+    shapes = [dict(lens=[5000], hq=32, hkv=8), dict(lens=[2100] * 128, hq=8, hkv=1),
+              dict(lens=[4000, 300, 2000], hq=8, hkv=2, d=64), dict(lens=[6000, 10], hq=16, hkv=2, d=256),
+              dict(lens=[2100] * 40, hq=8, hkv=2, kv="same", spread=1, alibi=True),
+              dict(lens=[700], hq=32, hkv=8, window=500)]
+    cases = []
+    for i, kw in enumerate(shapes):
+        kw = dict(kw)
+        cases.append(Case(210 + i, [(n - 1, 1) for n in kw.pop("lens")], **kw))
+    size = max(P.paged_attn_decode_ext_workspace_size(len(c.seq_lens), c.q.shape[1], c.k.shape[1],
+                                                      c.q.shape[2], c.max_ctx, c.window, part)
+               for c in cases for part in (0, 64))
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    want = [[c.decode(part) for part in (0, 64)] for c in cases]
+    for c, w in zip(cases, want):
+        for got in w:
+            c.check(got)
+    ok()
+    for order in ([0, 1, 0, 2, 1, 3, 4, 5, 1], [5, 4, 1, 3, 2, 0, 1, 1, 0]):
+        for i in order:
+            for part, w in zip((0, 64), want[i]):
+                got = cases[i].decode(part, workspace=ws)
+                assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+    ok()
+
+
+def test_graphs_of_other_sizes_share_a_workspace():
+    a = Case(220, [(6000, 1)], hq=32, hkv=8)
+    b = Case(221, [(2500, 1)] * 100, hq=4, hkv=1)
+    size = max(P.paged_attn_decode_ext_workspace_size(len(c.seq_lens), c.q.shape[1], c.k.shape[1],
+                                                      128, c.max_ctx) for c in (a, b))
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    want, graphs = [c.decode() for c in (a, b)], []
+    outs = [torch.zeros_like(c.q) for c in (a, b)]
+    for c, out in zip((a, b), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            P.paged_attn_decode_ext(out, c.q, c.k, c.v, c.tables, c.seq_lens, c.scale, c.max_ctx,
+                                    c.ks, c.vs, workspace=ws)
+        graphs.append(g)
+    for _ in range(4):
+        for i in (0, 1, 1, 0):
+            outs[i].zero_()
+            graphs[i].replay()
+            assert torch.equal(outs[i], want[i][0])
+    ok()
