@@ -445,7 +445,10 @@ pkv_status rope_append_block_scaled(const void* key, const void* value, pkv_dtyp
 /*
  * paged_attn_decode_ext_workspace_size — bytes of workspace that
  *   paged_attn_decode_ext needs (window as passed to it); 0 for invalid sizes.
- *   Query on the device that will run the call. Zero-fill the workspace once
+ *   Query on the device that will run the call. More sequences, a larger
+ *   max_seq_len or a larger window (none being the largest) never need less,
+ *   the heads, head_dim and partition_tokens being the same: a workspace made
+ *   for the largest call serves the smaller ones. Zero-fill the workspace once
  *   before its first use, and again after a call that ended with a device
  *   error; apart from that calls of paged_attn_decode_ext of any sizes may use
  *   it in turn, captured in graphs or not. (The other entry points with a

@@ -76,9 +76,8 @@ size_t paged_attn_decode_ext_workspace_size(int num_seqs, int num_q_heads, int n
       partition_tokens > kMaxPartitionTokens)
     return 0;
   // E4M3 caches have the most resident CTAs, hence the most partitions: enough for any
-  return plan_decode_ext(num_seqs, num_q_heads, num_kv_heads, head_dim,
-                         plan_span(max_seq_len, window), partition_tokens, true, sm_count())
-      .bytes;
+  return decode_ext_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                          plan_span(max_seq_len, window), partition_tokens, true, sm_count());
 }
 
 pkv_status paged_attn_decode_ext(void* out, const void* q, pkv_dtype q_dtype, const void* k_cache,
@@ -107,7 +106,9 @@ pkv_status paged_attn_decode_ext(void* out, const void* q, pkv_dtype q_dtype, co
   const DecodePlan pl = plan_decode_ext(num_seqs, num_q_heads, num_kv_heads, head_dim, span,
                                         partition_tokens, page_dtype == PKV_FP8_E4M3, sms);
   if (pl.max_parts > kMaxDecodeExtParts) return PKV_ERR_UNSUPPORTED;
-  if (workspace == nullptr || workspace_bytes < pl.bytes ||
+  const size_t need = decode_ext_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, span,
+                                       partition_tokens, page_dtype == PKV_FP8_E4M3, sms);
+  if (workspace == nullptr || workspace_bytes < need ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PKV_ERR_WORKSPACE;
   const int shift = page_shift(block_size), bs_log2 = block_log2(block_size);

@@ -20,6 +20,9 @@ inline int decode_ext_ctas_per_sm(int head_dim, bool e4m3) {
   return std::max(1, std::min(8, 227 * 1024 / smem));
 }
 
+// Tokens of a partition of `span` keys for a call alone on the GPU (below).
+inline int best_part(int span) { return std::max(64, (int)std::sqrt(16.0 * std::max(0, span))); }
+
 // Automatic partitions (partition_tokens = 0) of `span` keys:
 //  - A call alone on the GPU takes about a + b * part + c * parts: a CTA reads a
 //    token in b = 0.01 us (head_dim 128, E4M3), the merging CTA a partition in c =
@@ -39,7 +42,7 @@ inline DecodePlan plan_decode_ext(int num_seqs, int num_q_heads, int num_kv_head
     if (sms <= 0) sms = 148;
     const int64_t units = std::max<int64_t>(1, (int64_t)num_seqs * num_kv_heads);
     const int64_t resident = (int64_t)sms * decode_ext_ctas_per_sm(head_dim, e4m3);
-    const int best = std::max(64, (int)std::sqrt(16.0 * std::max(0, span)));
+    const int best = best_part(span);
     const int64_t parts =
         std::min<int64_t>(std::max(1, (span + best - 1) / best), std::max<int64_t>(1, resident / units));
     part = (int)std::min<int64_t>(2048, ((span + parts - 1) / parts + 15) / 16 * 16);
@@ -47,6 +50,30 @@ inline DecodePlan plan_decode_ext(int num_seqs, int num_q_heads, int num_kv_head
   }
   // (an explicit size: the same layout)
   return plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, span, part, sms);
+}
+
+// Bytes that paged_attn_decode_ext asks for: enough for its plan and for those of every
+// call with as many sequences and keys or fewer, so that a workspace made for the
+// largest batch serves the smaller ones, whose contexts are split into more parts.
+inline size_t decode_ext_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                               int span, int partition_tokens, bool e4m3, int sms) {
+  int64_t parts;                                   // of all sequences, a KV head
+  if (partition_tokens > 0) {
+    parts = num_seqs * std::max<int64_t>(1, ((int64_t)span + partition_tokens - 1) / partition_tokens);
+  } else {
+    if (sms <= 0) sms = 148;
+    const int64_t resident = (int64_t)sms * decode_ext_ctas_per_sm(head_dim, e4m3);
+    // the most parts of up to `span` keys: of these, or of the longest with the next
+    // smaller best part
+    const int64_t k = best_part(span), below = (k * k - 1) / 16;
+    int64_t most = std::max<int64_t>(1, ((int64_t)span + k - 1) / k);
+    if (k > 64) most = std::max(most, (below + k - 2) / (k - 1));
+    parts = std::max(std::min(num_seqs * most, std::max<int64_t>(num_seqs, resident / num_kv_heads)),
+                     num_seqs * (((int64_t)span + 2047) / 2048));
+  }
+  const size_t rows = (size_t)parts * num_q_heads;
+  return align256((size_t)num_seqs * num_kv_heads * 8) + align256(rows * head_dim * sizeof(float)) +
+         align256(rows * sizeof(float));
 }
 
 }  // namespace pkv

@@ -1,0 +1,26 @@
+"""Host side of the block-scaled append and the _ext attentions: workspace sizes; needs no GPU."""
+import pytest
+
+import paged_kv_decode_11_gb300 as P
+from paged_kv_decode_11_gb300 import build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return P.load()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (8, 8, 64), (16, 2, 256), (28, 4, 128)])
+@pytest.mark.parametrize("part", [0, 16, 512])
+def test_a_larger_call_has_a_larger_workspace(lib, Hq, Hkv, D, part):
+    size = P.paged_attn_decode_ext_workspace_size
+    batches, lens = (1, 2, 3, 7, 8, 16, 17, 40, 128, 300), (1, 64, 65, 300, 700, 1000, 4096, 8192, 131072)
+    table = [[size(b, Hq, Hkv, D, n, 0, part) for n in lens] for b in batches]
+    for row in table:
+        assert row == sorted(row)
+    for col in zip(*table):
+        assert list(col) == sorted(col)
+    for b in batches:
+        windows = [size(b, Hq, Hkv, D, 8192, w, part) for w in (1, 50, 51, 700, 5000, 8192, 0)]
+        assert windows == sorted(windows)

@@ -227,3 +227,12 @@ def test_graphs_of_other_sizes_share_a_workspace():
             graphs[i].replay()
             assert torch.equal(outs[i], want[i][0])
     ok()
+
+
+def test_a_workspace_for_a_large_batch_serves_the_smaller_ones():
+    ws = torch.zeros(P.paged_attn_decode_ext_workspace_size(64, 16, 2, 128, 3000), dtype=torch.uint8,
+                     device="cuda")
+    for n in (64, 50, 33, 8, 5, 2, 1):
+        c = Case(230 + n, [(2999, 1)] * n, hq=16, hkv=2)
+        c.check(c.decode(workspace=ws))
+    ok()
