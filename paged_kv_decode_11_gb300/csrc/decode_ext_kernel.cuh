@@ -493,7 +493,10 @@ __global__ void __launch_bounds__(NW * 32)
   for (int c0 = 0, ci = 0; c0 < nparts; c0 += CH, ++ci) {
     const int n = min(CH, nparts - c0);
     if (tid == 0) {
+      // the partials were written, and this shared memory read and written, through the
+      // generic proxy; the barrier above ordered both before these fences
       fence_proxy_async_global();
+      fence_proxy_async_smem();
       mbar_arrive_expect_tx(&s_mbar, (uint32_t)(G * n * D * 4));
       for (int hh = 0; hh < G; ++hh)
         bulk_load(s_o + hh * CH * D, p.ws_o + ((row0 + hh) * p.max_parts + c0) * D,

@@ -549,9 +549,11 @@ __global__ void __launch_bounds__(NW * 32)
     const int n = min(CH, nparts - c0);
     if (tid == 0) {
       // the partials were written through the generic proxy; the acquire
-      // above ordered them before this thread's reads, and this fence before
-      // its bulk copies
+      // above ordered them before this thread's reads, and the first fence before
+      // its bulk copies. The second orders what the CTA read and wrote in the space
+      // that they fill, up to the barrier above
       fence_proxy_async_global();
+      fence_proxy_async_smem();
       mbar_arrive_expect_tx(&s_mbar, (uint32_t)(G * n * D * 4));
       for (int hh = 0; hh < G; ++hh)
         bulk_load(s_o + hh * CH * D, p.ws_o + ((row0 + hh) * p.max_parts + c0) * D,

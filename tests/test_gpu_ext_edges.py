@@ -236,3 +236,16 @@ def test_a_workspace_for_a_large_batch_serves_the_smaller_ones():
         c = Case(230 + n, [(2999, 1)] * n, hq=16, hkv=2)
         c.check(c.decode(workspace=ws))
     ok()
+
+
+@pytest.mark.parametrize("kw", [dict(hq=16, hkv=1), dict(hq=8, hkv=1, d=256), dict(hq=7, hkv=1, d=64)])
+def test_merges_of_many_chunks_repeat_themselves(kw):
+    # hundreds of partitions: the merging CTA refills one staging space many times, right behind
+    # its own use of it
+    c = Case(240, [(5999, 1), (4000, 1), (777, 1)], **kw)
+    first = c.decode(16)
+    c.check(first)
+    for _ in range(50):
+        again = c.decode(16)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    ok()
