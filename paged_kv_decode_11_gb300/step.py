@@ -218,7 +218,8 @@ class BlockScaledStep:
     q, new_k, new_v: [tokens, heads, D] of all sequences in order, cu_q_lens [n + 1] their
     offsets, seq_lens including the new tokens. run() works on the buffers given here, so it
     can be captured into a CUDA graph and replayed with new contents: max_seq_len bounds the
-    decode sequences' contexts and max_q_len the chunks, at every replay."""
+    decode sequences' contexts and max_q_len the chunks (needed where there are sequences
+    behind the first num_decode), at every replay."""
 
     def __init__(self, k_cache, v_cache, k_scales, v_scales, q, new_k, new_v, block_tables,
                  seq_lens, cu_q_lens, num_decode, scale, max_seq_len, max_q_len=0, cos_sin=None,
@@ -229,6 +230,8 @@ class BlockScaledStep:
         self.block_tables, self.seq_lens, self.cu_q_lens = block_tables, seq_lens, cu_q_lens
         self.num_decode, self.scale = int(num_decode), float(scale)
         self.max_seq_len, self.max_q_len = int(max_seq_len), int(max_q_len)
+        if self.num_decode < seq_lens.shape[0] and self.max_q_len <= 0:
+            raise ValueError("max_q_len is needed for the sequences behind the first num_decode")
         self.cos_sin, self.neox_style = cos_sin, neox_style
         self.opts = dict(softcap=softcap, window=window, alibi_slopes=alibi_slopes)
         # the queries as attention takes them: rotated, or as they come

@@ -1,4 +1,4 @@
-"""Host side of the block-scaled append and the _ext attentions: workspace sizes; needs no GPU."""
+"""Host side of the block-scaled append, the _ext attentions and their step; needs no GPU."""
 import pytest
 
 import paged_kv_decode_11_gb300 as P
@@ -24,3 +24,17 @@ def test_a_larger_call_has_a_larger_workspace(lib, Hq, Hkv, D, part):
     for b in batches:
         windows = [size(b, Hq, Hkv, D, 8192, w, part) for w in (1, 50, 51, 700, 5000, 8192, 0)]
         assert windows == sorted(windows)
+
+
+def test_a_step_with_chunks_needs_their_bound():
+    import torch
+    from paged_kv_decode_11_gb300.step import BlockScaledStep
+    c = torch.zeros(4, 2, 16, 128, dtype=torch.uint8)
+    s, q, kv = torch.zeros(4, 2, dtype=torch.uint8), torch.zeros(6, 8, 128), torch.zeros(6, 2, 128)
+    t, lens = torch.zeros(2, 2, dtype=torch.int32), torch.tensor([9, 5], dtype=torch.int32)
+    cu = torch.tensor([0, 1, 6], dtype=torch.int32)
+    for bound in ({}, dict(max_q_len=0), dict(max_q_len=-1)):
+        with pytest.raises(ValueError, match="max_q_len"):
+            BlockScaledStep(c, c, s, s, q, kv, kv, t, lens, cu, 1, 0.1, 32, **bound)
+    BlockScaledStep(c, c, s, s, q, kv, kv, t, lens, cu, 1, 0.1, 32, max_q_len=5)
+    BlockScaledStep(c, c, s, s, q[:2], kv[:2], kv[:2], t, lens, cu, 2, 0.1, 32)
