@@ -500,7 +500,9 @@ pkv_status paged_attn_decode_ext(void* out, const void* q, pkv_dtype q_dtype,
  *   0 none. A row sees j < seq_lens[n] with j <= pos or j < prefix_lens[n],
  *   and, with a window, pos - j < window; the distance of the bias is
  *   |pos - j|. Blocks outside every row's window are not read.
- *   A chunk with L_n > max_q_len sets PKV_DEVERR_QLEN and is skipped.
+ *   A chunk with L_n > max_q_len sets PKV_DEVERR_QLEN and is skipped, with
+ *   max_q_len = 0 every chunk that has rows (out = NULL is fine then, and the
+ *   call does nothing).
  *   Everything else as paged_attn_prefill_chunk and paged_attn_decode_ext.
  */
 pkv_status paged_attn_prefill_chunk_ext(void* out, const void* q, pkv_dtype q_dtype,

@@ -175,7 +175,8 @@ pkv_status paged_attn_prefill_chunk_ext(void* out, const void* q, pkv_dtype q_dt
   if (total_q_tokens < 0 || max_q_len < 0) return PKV_ERR_INVALID_ARG;
   pkv_status st = check_attn(q_dtype, kv_dtype, num_seqs, num_q_heads, num_kv_heads, head_dim,
                              block_size, max_blocks_per_seq, num_blocks, scale, softcap, window);
-  if (st != PKV_OK || num_seqs == 0 || total_q_tokens == 0 || max_q_len == 0) return st;
+  if (st != PKV_OK || num_seqs == 0 || total_q_tokens == 0) return st;
+  if (max_q_len == 0 && out == nullptr) return PKV_OK;   // no chunk, and nowhere to put one
   if (!block_tables || !seq_lens || !cu_q_lens) return PKV_ERR_INVALID_ARG;
   st = check_tensors(out, q, k_cache, v_cache, kv_dtype, k_scales, v_scales);
   if (st != PKV_OK) return st;
@@ -214,7 +215,8 @@ pkv_status paged_attn_prefill_chunk_ext(void* out, const void* q, pkv_dtype q_dt
   p.G = G;
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
-  // no chunk is longer than the rows there are
+  // no chunk is longer than the rows there are (with 0 every chunk that has a row is
+  // flagged)
   p.max_q_len = std::min(max_q_len, total_q_tokens);
   p.q_rows = total_q_tokens;
   p.ppb_shift = shift;

@@ -1329,7 +1329,8 @@ struct PrefillTcLaunch {
     const pkv_status st = prepare(dev);
     if (st != PKV_OK) return st;
     const PrefillParams& q = prefill_base(ep);
-    const int tiles = (q.max_q_len + q.q_tile - 1) / q.q_tile;
+    // (one at least: its CTAs look every sequence over, where no chunk may have a row too)
+    const int tiles = std::max(1, (q.max_q_len + q.q_tile - 1) / q.q_tile);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     config(cfg, attr, dim3(tiles * SPLIT, q.Hkv, q.num_seqs), stream);

@@ -249,3 +249,16 @@ def test_merges_of_many_chunks_repeat_themselves(kw):
         again = c.decode(16)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
     ok()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(kv="same", spread=1, softcap=9.0), dict(kv="head", window=9)])
+def test_prefill_without_a_bound_flags_every_chunk(kw):
+    c = Case(250, [(50, 10), (300, 0), (0, 3)], **kw)
+    out, lse = c.prefill(max_q_len=0)
+    torch.cuda.synchronize()
+    assert P.pkv_get_device_error() == 0x10         # PKV_DEVERR_QLEN
+    assert (out == 9).all() and (lse == 9).all()
+    c = Case(251, [(50, 0), (0, 0)], pad=4, **kw)    # rows, but no chunk has one
+    out, _ = c.prefill(max_q_len=0)
+    ok()
+    assert (out == 9).all()
