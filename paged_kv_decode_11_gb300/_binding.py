@@ -137,6 +137,21 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
+def _workspace(size: int, device: torch.device, stream) -> torch.Tensor:
+    """A zero-filled workspace of one call's own, made on the stream that the call runs on: the
+    fill comes before the call, and what takes the memory afterwards comes behind it."""
+    def make():
+        return torch.zeros(max(size, 256), dtype=torch.uint8, device=device)
+    if stream is None:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle else
+                  torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return make()
+
+
 def _check(fn: str, status: int):
     if status != 0:
         raise PkvError(fn, status)
@@ -165,7 +180,7 @@ def paged_attn_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
     assert block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32
     if workspace is None:
         ws = paged_attn_decode_workspace_size(B, Hq, hkv, D, max_seq_len, partition_tokens)
-        workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(ws, q.device, stream)
     st = load().paged_attn_decode(
         _dev_ptr(out, "out"), _dev_ptr(q, "q"), dtype_code(q), _dev_ptr(k_cache, "k_cache"),
         _dev_ptr(v_cache, "v_cache"), dtype_code(k_cache), _dev_ptr(block_tables, "block_tables"),
@@ -197,7 +212,7 @@ def paged_attn_decode_step(key: torch.Tensor, value: torch.Tensor, slot_mapping:
     assert block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32
     if workspace is None:
         ws = paged_attn_decode_workspace_size(B, Hq, hkv, D, max_seq_len, partition_tokens)
-        workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(ws, q.device, stream)
     st = load().paged_attn_decode_step(
         _dev_ptr(key, "key"), _dev_ptr(value, "value"), _dev_ptr(slot_mapping, "slot_mapping"),
         _dev_ptr(out, "out"), _dev_ptr(q, "q"), dtype_code(q), _dev_ptr(k_cache, "k_cache"),
@@ -283,7 +298,7 @@ def paged_attn_varlen(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
     if workspace is None:
         ws = paged_attn_decode_workspace_size(num_decode_seqs, Hq, hkv, D, max_decode_seq_len,
                                               partition_tokens)
-        workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(ws, q.device, stream)
     st = load().paged_attn_varlen(
         _dev_ptr(out, "out"), _dev_ptr(q, "q"), dtype_code(q), _dev_ptr(k_cache, "k_cache"),
         _dev_ptr(v_cache, "v_cache"), dtype_code(k_cache), _dev_ptr(block_tables, "block_tables"),
@@ -390,7 +405,7 @@ def paged_attn_decode_ext(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Ten
         B, Hq, D = q.shape
         ws = paged_attn_decode_ext_workspace_size(B, Hq, k_cache.shape[1], D, max_seq_len, window,
                                                   partition_tokens)
-        workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(ws, q.device, stream)
     st = _native.decode_ext(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len,
                             k_scales, v_scales, softcap, window, alibi_slopes, partition_tokens,
                             out_lse, workspace, _handle(stream))

@@ -262,3 +262,40 @@ def test_prefill_without_a_bound_flags_every_chunk(kw):
     out, _ = c.prefill(max_q_len=0)
     ok()
     assert (out == 9).all()
+
+
+@pytest.mark.parametrize("handle", [lambda s: s, lambda s: s.cuda_stream, lambda s: 0, lambda s: None])
+def test_a_workspace_of_the_calls_own_lives_on_its_stream(handle, monkeypatch):
+    # without a workspace argument: filled, and given back, in the order of the stream that the call
+    # runs on, whichever stream is current
+    c = Case(260, [(5000, 1), (800, 1)])
+    old = Case(261, [(5000, 1), (800, 1)], kv="same", spread=1)
+    key, slots = torch.randn(2, 2, 128, device="cuda").bfloat16(), torch.full((2,), -1, device="cuda")
+    qsl = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    want = {s: s, 0: torch.cuda.default_stream()}.get(handle(s), s)
+    if handle(s) is None:
+        want = torch.cuda.current_stream()
+    seen, zeros = [], torch.zeros
+
+    def watched(*a, **kw):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return zeros(*a, **kw)
+    out = torch.empty_like(c.q)
+    args = (old.q, old.k, old.v, old.tables, old.seq_lens)
+    olds = [torch.empty_like(old.q) for _ in range(3)]
+    ref, plain = c.decode(), old.decode()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "zeros", watched)
+    P.paged_attn_decode_ext(out, c.q, c.k, c.v, c.tables, c.seq_lens, c.scale, c.max_ctx, c.ks, c.vs,
+                            stream=handle(s))
+    P.paged_attn_decode(olds[0], *args, old.scale, old.max_ctx, stream=handle(s))
+    P.paged_attn_decode_step(key, key, slots, olds[1], *args, old.scale, old.max_ctx, stream=handle(s))
+    P.paged_attn_varlen(olds[2], *args, qsl, 2, old.scale, 0, old.max_ctx, stream=handle(s))
+    junk = [torch.full((1 << 20,), 1.5, device="cuda") for _ in range(50)]     # the current stream's memory
+    ok()
+    assert seen == [want.cuda_stream] * 4 and len(junk) == 50
+    assert torch.equal(out, ref[0])
+    tol = R.tolerance(old.want(), old.q.dtype, old.p_dtype)
+    for x in olds:
+        assert ((x.double() - plain[0].double()).abs() <= 2 * tol).all()
