@@ -15,6 +15,8 @@ from typing import Optional
 
 import torch
 
+from .build import native_target
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpkv.so")
 
@@ -35,6 +37,7 @@ EXPORTS = ("paged_attn_decode_workspace_size", "paged_attn_decode", "paged_attn_
 
 _lib = None
 _native = None
+_native_error = None
 
 
 class PkvError(RuntimeError):
@@ -49,7 +52,7 @@ class PkvError(RuntimeError):
 
 def load(path: str = LIB_PATH):
     """Load libpkv.so and declare its signatures. Raises if it is absent."""
-    global _lib, _native
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -97,16 +100,38 @@ def load(path: str = LIB_PATH):
     L.pkv_status_string.argtypes = [I]
     L.pkv_selftest_bounded_wait.restype = I
     L.pkv_selftest_bounded_wait.argtypes = [ctypes.c_uint, P]
+    _lib = L
+    _load_native()
+    return L
+
+
+def _load_native() -> None:
+    """Bind the _native module to the library. Without one for this torch and Python only the
+    calls that go through it fail."""
+    global _native, _native_error
     try:
         from . import _native as native
+        if native.built_for != native_target():
+            raise ImportError(f"it was built for {native.built_for}, this is {native_target()}")
     except ImportError as e:
-        raise RuntimeError("_native not built; run paged_kv_decode_11_gb300.build.build()") from e
-    native.bind(*[ctypes.cast(f, P).value for f in (L.paged_attn_decode_ext,
-                                                    L.paged_attn_prefill_chunk_ext,
-                                                    L.rope_append_block_scaled)])
+        _native_error = e
+        return
+    native.bind(*[ctypes.cast(f, ctypes.c_void_p).value
+                  for f in (_lib.paged_attn_decode_ext, _lib.paged_attn_prefill_chunk_ext,
+                            _lib.rope_append_block_scaled)])
     _native = native
-    _lib = L
-    return L
+
+
+def _marshal():
+    """The _native module, for the calls that go through it."""
+    if _native is None:
+        load()
+    if _native is None:
+        _load_native()
+    if _native is None:
+        raise RuntimeError("no _native module for this torch and Python; run "
+                           "paged_kv_decode_11_gb300.build.build()") from _native_error
+    return _native
 
 
 def dtype_code(t: torch.Tensor) -> int:
@@ -373,10 +398,9 @@ def rope_append_block_scaled(key: torch.Tensor, value: torch.Tensor, k_cache: to
     v_scales: uint8 or float8_e8m0fnu [num_blocks, Hkv]). With cos_sin_cache fp32
     [max_position, rot_dim] the keys are rotated on the way, and query [T, Hq, D] into
     query_out (in place without one)."""
-    if _native is None:
-        load()
-    st = _native.append(key, value, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens,
-                        cu_q_lens, query, query_out, cos_sin_cache, neox_style, _handle(stream))
+    native = _native or _marshal()
+    st = native.append(key, value, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens,
+                       cu_q_lens, query, query_out, cos_sin_cache, neox_style, _handle(stream))
     _check("rope_append_block_scaled", st)
 
 
@@ -399,16 +423,15 @@ def paged_attn_decode_ext(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Ten
     distance (alibi_slopes fp32 [Hq]) or limited to the last `window` keys; k_scales/v_scales
     uint8 or float8_e8m0fnu [num_blocks, Hkv] (block scales) or fp32 [Hkv] with an E4M3 cache.
     Workspace rule as paged_attn_decode (paged_attn_decode_ext_workspace_size bytes)."""
-    if _native is None:
-        load()
+    native = _native or _marshal()
     if workspace is None:
         B, Hq, D = q.shape
         ws = paged_attn_decode_ext_workspace_size(B, Hq, k_cache.shape[1], D, max_seq_len, window,
                                                   partition_tokens)
         workspace = _workspace(ws, q.device, stream)
-    st = _native.decode_ext(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len,
-                            k_scales, v_scales, softcap, window, alibi_slopes, partition_tokens,
-                            out_lse, workspace, _handle(stream))
+    st = native.decode_ext(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len,
+                           k_scales, v_scales, softcap, window, alibi_slopes, partition_tokens,
+                           out_lse, workspace, _handle(stream))
     _check("paged_attn_decode_ext", st)
 
 
@@ -423,11 +446,10 @@ def paged_attn_prefill_chunk_ext(out: torch.Tensor, q: torch.Tensor, k_cache: to
     """out[T, Hq, D] <- chunked-prefill attention of q[T, Hq, D] with the options of
     paged_attn_decode_ext, and prefix_lens int32 [n]: positions below it are seen by every row
     of their sequence."""
-    if _native is None:
-        load()
-    st = _native.prefill_ext(out, q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale,
-                             max_q_len, k_scales, v_scales, softcap, window, alibi_slopes,
-                             prefix_lens, out_lse, _handle(stream))
+    native = _native or _marshal()
+    st = native.prefill_ext(out, q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale,
+                            max_q_len, k_scales, v_scales, softcap, window, alibi_slopes,
+                            prefix_lens, out_lse, _handle(stream))
     _check("paged_attn_prefill_chunk_ext", st)
 
 

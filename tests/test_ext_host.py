@@ -38,3 +38,50 @@ def test_a_step_with_chunks_needs_their_bound():
             BlockScaledStep(c, c, s, s, q, kv, kv, t, lens, cu, 1, 0.1, 32, **bound)
     BlockScaledStep(c, c, s, s, q, kv, kv, t, lens, cu, 1, 0.1, 32, max_q_len=5)
     BlockScaledStep(c, c, s, s, q[:2], kv[:2], kv[:2], t, lens, cu, 2, 0.1, 32)
+
+
+def _elsewhere(tmp_path, code, without_native):
+    """Runs code where a copy of the built package lies, with or without its _native module."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    src = os.path.dirname(os.path.abspath(build.__file__))
+    shutil.copytree(src, tmp_path / "paged_kv_decode_11_gb300", ignore=shutil.ignore_patterns(
+        "csrc", "_build", "__pycache__", *(["_native.so"] if without_native else [])))
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
+    return r.stdout.split("\n")
+
+
+OLD_CALLS = """
+import paged_kv_decode_11_gb300 as P
+from paged_kv_decode_11_gb300 import _binding
+{before}
+L = P.load()
+print(P.pkv_status_string(3), P.paged_attn_decode_workspace_size(4, 8, 2, 128, 128, 64),
+      P.paged_attn_decode_ext_workspace_size(4, 8, 2, 128, 128, 0, 64))
+try:
+    P.rope_append_block_scaled(*[None] * 9)
+except RuntimeError as e:
+    print(e, e.__cause__)
+"""
+
+
+def test_old_calls_need_no_native_module(lib, tmp_path):
+    size = P.paged_attn_decode_workspace_size(4, 8, 2, 128, 128, 64)
+    out = _elsewhere(tmp_path, OLD_CALLS.format(before=""), True)
+    assert str(size) in out[0] and "build.build()" in out[1]
+
+
+def test_a_native_module_for_another_torch_is_not_used(lib, tmp_path):
+    before = "_binding.native_target = lambda: 'torch 0.1, Python 3.0, other'"
+    out = _elsewhere(tmp_path, OLD_CALLS.format(before=before), False)
+    assert str(P.paged_attn_decode_workspace_size(4, 8, 2, 128, 128, 64)) in out[0]
+    assert "built for " + build.native_target() in out[1] and "torch 0.1" in out[1]
+
+
+def test_build_sees_that_torch_changed(lib, monkeypatch):
+    assert build.up_to_date()
+    monkeypatch.setattr(build, "native_target", lambda: "torch 0.1, Python 3.0, other")
+    assert build.lib_up_to_date() and not build.native_up_to_date() and not build.up_to_date()
