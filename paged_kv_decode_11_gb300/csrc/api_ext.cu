@@ -21,9 +21,11 @@ namespace {
 constexpr float kLog2eHost = 1.4426950408889634f;
 
 // Keys a decode plan has to cover: with a window, its keys and those before them
-// on the first one's 16-token page.
+// on the first one's 16-token page; never more than a table's row holds
+// (page_rows_fit), so that the plan's sums stay in 32 bits.
 int plan_span(int max_seq_len, int window) {
-  return window > 0 ? (int)std::min<int64_t>(max_seq_len, (int64_t)window + 15) : max_seq_len;
+  const int64_t span = std::min(max_seq_len, 1 << 30);
+  return (int)(window > 0 ? std::min<int64_t>(span, (int64_t)window + 15) : span);
 }
 
 bool valid_ext_dtypes(pkv_dtype q, pkv_dtype kv) {

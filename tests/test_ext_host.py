@@ -85,3 +85,15 @@ def test_build_sees_that_torch_changed(lib, monkeypatch):
     assert build.up_to_date()
     monkeypatch.setattr(build, "native_target", lambda: "torch 0.1, Python 3.0, other")
     assert build.lib_up_to_date() and not build.native_up_to_date() and not build.up_to_date()
+
+
+@pytest.mark.parametrize("part", [0, 512])
+def test_bounds_above_the_longest_table(lib, part):
+    # a row of a block table holds less than 2^30 tokens: a larger bound plans for no more, and the
+    # 32-bit sums behind it do not wrap
+    size = P.paged_attn_decode_ext_workspace_size
+    top = size(1, 8, 2, 128, 2 ** 30, 0, part)
+    parts = 2 ** 30 // (part or 2048)
+    assert top >= parts * 8 * (4 * 128 + 4)
+    for n in (2 ** 30 + 1, 2 ** 31 - 1000, 2 ** 31 - 1):
+        assert size(1, 8, 2, 128, n, 0, part) == size(1, 8, 2, 128, n, n, part) == top
