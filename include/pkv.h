@@ -147,7 +147,9 @@ size_t paged_attn_decode_workspace_size(int num_seqs, int num_q_heads,
  *   so a call enqueues nothing but its kernel. A call that ends with a
  *   device error may leave counters set; zero the workspace again before
  *   reusing it (PKV_DEVERR_COUNTER reports counters found non-zero). Two
- *   calls that share a workspace must not overlap on the GPU.
+ *   calls that share a workspace must not overlap on the GPU, and are calls of
+ *   the same num_seqs and num_kv_heads (others' partial results lie where
+ *   these counters do; zero it in between, or give each its own).
  *   The kernel is launched as a programmatic dependent of the kernel ahead
  *   of it on `stream`: it may become resident while that kernel runs, and
  *   reads no input before that kernel has finished.
@@ -421,6 +423,7 @@ pkv_status rope_reshape_and_cache(void* query, const void* key, const void* valu
  *           to a midpoint of src_dtype, may differ by a step between the calls.)
  *   query, query_out: [total_q_tokens, Hq, D] src_dtype, the rotated queries;
  *           query_out may be query itself (in place), or both NULL.
+ *   A stored scale of 255 (NaN) counts as 254, the codes beside it as they are.
  *   A block that the call writes belongs to one sequence: copy a shared,
  *   partly filled block before appending to it. (Two sequences that write one
  *   block leave its contents undefined, nothing else.)
@@ -474,7 +477,10 @@ size_t paged_attn_decode_ext_workspace_size(int num_seqs, int num_q_heads, int n
  *   [Hq]) leave a step out. Blocks wholly outside a sequence's window are not
  *   read, and their block table entries may hold anything.
  *   scale is positive and finite, softcap finite. seq_lens[b] == 0 gives
- *   out = 0, lse = -inf. BS 16, 32 or 64; everything else as
+ *   out = 0, lse = -inf. A NaN score (from q, K or a K scale of 255) makes the
+ *   row's out and lse NaN, a V scale of 255 its out. (With a bf16 q over an E4M3
+ *   cache a KV head's queries are scaled together: a NaN or infinity in one
+ *   leaves the results of the others without meaning.) BS 16, 32 or 64; everything else as
  *   paged_attn_decode (a workspace of paged_attn_decode_ext_workspace_size()
  *   bytes, partition_tokens, errors, programmatic launch), but for contexts cut
  *   into more than 2^23 partitions, which are PKV_ERR_UNSUPPORTED.
@@ -499,7 +505,10 @@ pkv_status paged_attn_decode_ext(void* out, const void* q, pkv_dtype q_dtype,
  *   attends both ways); values past seq_lens[n] mean the whole context, below
  *   0 none. A row sees j < seq_lens[n] with j <= pos or j < prefix_lens[n],
  *   and, with a window, pos - j < window; the distance of the bias is
- *   |pos - j|. Blocks outside every row's window are not read.
+ *   |pos - j|. Blocks outside every row's window are not read. A NaN or an
+ *   infinity in V may also reach rows that do not see its key, of the tokens
+ *   that share a query tile (128 / G tokens) with one that does, as in
+ *   paged_attn_prefill_chunk.
  *   A chunk with L_n > max_q_len sets PKV_DEVERR_QLEN and is skipped, with
  *   max_q_len = 0 every chunk that has rows (out = NULL is fine then, and the
  *   call does nothing).

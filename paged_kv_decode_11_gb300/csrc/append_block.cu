@@ -25,19 +25,21 @@
 // values. A group holds 2 x 16 elements of the run per thread in registers from
 // the maximum to the codes; of a longer run (more than 32 tokens at head_dim 128)
 // what was not kept is loaded and rotated again (holding 4 x 16 spilled registers
-// and left room for fewer CTAs: 2,039 tokens of 24 / 8 heads 14.9 us, 13.2 with 2). No two CTAs touch one block and
-// head, so nothing is atomic and the result does not depend on scheduling. The
-// queries follow in the same grid: one warp or a few take a row, a thread keeps the
-// angles of its 16 dims and goes over the row's heads.
+// and left room for fewer CTAs: 2,039 tokens of 24 / 8 heads 14.9 us, 13.2 with 2). No two
+// CTAs touch one block and head, so nothing is atomic and the result does not depend on
+// scheduling. The queries follow in the same grid: one warp or up to eight take a row, a
+// thread keeps the angles of its 16 dims and goes over the row's heads.
 //
-// Bound: bytes (16-bit rows in, 8-bit codes out, queries in and out) when the call is
-// long: 7 chunks of 150 to 2,100 tokens, 28 / 4 heads, D = 128, f16, half of each head
-// rotated: 139 MB in 35 us, 4.0 TB/s (a plain copy of its queries alone, 113 MB, takes
-// 36.9; 41.6 us with a warp's loads waiting for the stores before them, 91 with a
-// CTA per row and doubles for the undecided sums). For the tokens of a decode batch
+// Bound: when the call is long, the latency of its loads at the 24 warps that an SM holds:
+// the chunk kernels are kept to 80 registers a thread for that, and spill 120 to 136 bytes
+// (47.4 us with two CTAs an SM, 43.8 with three and two heads in flight). 7 chunks of 150 to 2,100
+// tokens, 28 / 4 heads, D = 128, f16, half of each head rotated: 139 MB in 35 us, 4.0 TB/s
+// of algorithmic bytes, DRAM 36 % busy; a tensor copy of as many bytes takes 44.6 us.
+// (41.6 us with a warp's loads waiting for the stores before them, 91 with a CTA per row
+// and doubles for the undecided sums.) For the tokens of a decode batch
 // the chain of loads before the first store (sequence, block id, scale) is what
 // takes the time, so everything that can be addressed without them is loaded first:
-// 128 tokens of 32 / 8 heads 5.5 us, one token 2.9.
+// 128 tokens of 32 / 8 heads 5.4 us, one token 2.6.
 #include "block_scale.cuh"
 #include "f32x2.cuh"
 #include "rope.cuh"
@@ -269,7 +271,8 @@ __global__ void __launch_bounds__(2 * GROUP, GROUP == kLongGroup ? 3 : 8)
       const int count = run << items_log2;
       const int id = p.block_tables[(int64_t)n * p.max_blocks + (pos >> p.bs_log2)];
       const uint16_t* rows = src + ((int64_t)row * p.Hkv + h << p.d_log2);
-      // items t, t + 128, .. of chunk base .. base + 511 of the run, rotated
+      // items base + t and base + t + kGroup of the run (its chunk of kKeep * kGroup items from
+      // base on), rotated
       Pair8 x[kKeep];
       auto take = [&](int base) {
 #pragma unroll

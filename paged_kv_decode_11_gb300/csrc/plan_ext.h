@@ -12,8 +12,10 @@ namespace pkv {
 // than the bits of any normal one.
 constexpr int kMaxDecodeExtParts = 1 << 23;
 
-// CTAs of kDecodeWarps warps an SM holds: the rings (3 stages of E4M3 pages or 2
-// of 16-bit ones per warp, K and V) are what bounds them, 8 at most.
+// CTAs of kDecodeWarps warps an SM holds by the shared memory of their rings (3 stages of
+// E4M3 pages or 2 of 16-bit ones per warp, K and V), 8 at most. Registers hold fewer at
+// head_dim 64 (7 of E4M3 pages; with more than 8 heads to a KV head 4) and, with more
+// than 8, at 128 (2 of 4): such a call may take a second wave, which costs time alone.
 inline int decode_ext_ctas_per_sm(int head_dim, bool e4m3) {
   const int page = 16 * head_dim * (e4m3 ? 1 : 2);
   const int smem = 4096 + kDecodeWarps * (e4m3 ? 3 : 2) * 2 * page;
@@ -27,7 +29,7 @@ inline int best_part(int span) { return std::max(64, (int)std::sqrt(16.0 * std::
 //  - A call alone on the GPU takes about a + b * part + c * parts: a CTA reads a
 //    token in b = 0.01 us (head_dim 128, E4M3), the merging CTA a partition in c =
 //    0.1 to 0.16 us, so parts of sqrt(16 span) tokens cost least (one sequence, 8
-//    KV heads: 700 keys 11.4 us in parts of 512, 6.9 in parts of 112; 4,000 keys
+//    KV heads: 700 keys 11.4 us in parts of 512, 7.4 in parts of 112; 4,000 keys
 //    11.8 in 512, 9.1 in 256; 32,000 keys 23.6 in 512, 22.6 in 1,024);
 //  - but no more parts than keep every CTA resident at once, while one wave can
 //    hold the call: a second wave that is mostly empty costs as much as the first

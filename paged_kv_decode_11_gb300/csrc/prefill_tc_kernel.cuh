@@ -1,8 +1,8 @@
 // prefill_tc_kernel.cuh — causal chunked-prefill attention on the
 // fifth-generation tensor cores (tcgen05): 16-bit caches at head_dim 64, 128
-// and 256, E4M3 caches at 64 and 128. Instantiated by prefill_tc.cu, and with
-// block scales and modified scores (MODE) by prefill_block.cu and
-// prefill_mod.cu.
+// and 256, E4M3 caches at 64 and 128, and with MODE at 256 too. Instantiated by
+// prefill_tc.cu, and with block scales and modified scores (MODE) by
+// prefill_block.cu and prefill_mod.cu.
 //
 // Follows "Chunked Prefill" (Litellama, Features: a long prompt enters the
 // batch as chunks of new query tokens attending their cached context) with
@@ -81,17 +81,19 @@ constexpr int kTcPlain = 0, kTcBlockScales = 1, kTcModScores = 2;   // MODE bits
 // The MODE kernels always run alone, in 128-key tiles up to D = 128, with two
 // softmax groups over one S buffer each: their softmax has more work per key (scales
 // per page, rewritten scores), so one group's runs while the other's products do.
-// Long chunk of block scales (2,048 on 4,096, 32 / 8 heads, D = 128): 291 us, 591
-// TFLOP/s; with one group over three buffers 302, two groups over 64-key tiles 358. The producers of an E4M3
-// operand split a tile by pages (SHARE), each staging and converting its own; with
-// one converting warp per operand that chunk took 558 us. At D = 256 the P in tensor
+// Long chunk of block scales (2,048 on 4,096, 32 / 8 heads, D = 128): 275 us, 625
+// TFLOP/s (291 when these were compared: one group over three buffers 302, two groups
+// over 64-key tiles 358). The producers of an E4M3 operand split a tile by pages (SHARE),
+// each staging and converting its own; with one converting warp per operand
+// that chunk took 558 us. At D = 256 the P in tensor
 // memory leaves an E4M3 cache's staging room beside the query tile, and the seven
 // producers are worth having with a 16-bit one too (2,048 on 4,096 at Hq 16 / Hkv 8
 // with a bias: 285 us with one per operand, 239 with seven).
 template <int D, int NST, bool KV8 = false, bool ALONE = true, int MODE = kTcPlain>
 struct PrefillTcCfg {
-  // 128-key tiles (WIDE): one softmax group over two S buffers in tensor
-  // memory, P written over its own S; otherwise two groups up to D = 128
+  // 128-key tiles (WIDE): one softmax group over three S buffers in tensor
+  // memory, or with MODE two groups over one each, P written over its own S;
+  // otherwise two groups up to D = 128
   static constexpr bool WIDE = D <= 128 && (MODE != kTcPlain || (ALONE && !KV8));
   static constexpr bool SHARE = KV8 && MODE != kTcPlain;
   static constexpr int NG = WIDE ? (MODE == kTcPlain ? 1 : 2) : (D <= 128 ? 2 : 1);
@@ -138,7 +140,7 @@ struct PrefillTcCfg {
   static constexpr int STG_BYTES = PAGES * STG_PAGE;         // one staged E4M3 tile
   static constexpr int SMEM_BYTES =
       1024 + Q_BYTES + 2 * RING_BYTES + (PTM ? 0 : NSB * NG * P_BYTES) + 2 * NSS * STG_BYTES;
-  static constexpr uint32_t TMEM_COLS = 512;                  // 2 S buffers and O per group
+  static constexpr uint32_t TMEM_COLS = 512;                  // NSB S buffers and O per group
   static_assert(NG * (NSB * KEYS + D) <= (int)TMEM_COLS, "tensor memory");
 };
 
@@ -152,7 +154,8 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
 }
 
 // 2^x by the SFU's approximation (flushes subnormal results to 0; 2^-inf = 0).
-// Softmax weights here lie in [0, 2^8] and are rounded to 16 bits next.
+// Softmax weights here lie in [0, 2^8], with MODE in [0, 2^15], and are rounded to
+// 16 bits next.
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -861,8 +864,8 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
       // A row's scores, CH keys at a time, twice: rewritten (MOD) or as they are for
       // the maxima, then for P. The loops are not unrolled: a row's worth of
       // straight-line code beside the producers' does not stay in the instruction
-      // caches (CH = 32 291 us on the long chunk; two chunks unrolled, the second
-      // on its way from tensor memory meanwhile, 326; CH = 16 319).
+      // caches (on the long chunk at the time, CH = 32 291 us; two chunks unrolled, the
+      // second on its way from tensor memory meanwhile, 326; CH = 16 319).
       constexpr int CH = 32, NCH = kTcKeys / CH, PPC = CH / kBS;
       float x[CH], kf[PPC], ev[PPC];
       if constexpr (BSC) {
@@ -984,7 +987,10 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
       // 2^-back, back = w_ref - ev - m_ref: relative to O's reference, with the page's
       // V scale in it. A page whose V scale is so small that its P would leave fp32
       // (back above 80: its part of O is nothing) keeps a P of 2^-80 times the
-      // probabilities, 0 in f16, so that its sum stays exact.
+      // probabilities, 0 in f16, so that its sum stays exact. P is rounded to the MMAs'
+      // 16-bit type, by half a step at most (bf16 2^-8, f16 2^-11 of a weight; the sum
+      // takes them unrounded): its low half would be a second P.V product, half as many
+      // MMAs again, for a bf16 result that is itself rounded by 2^-8.
       const float ms = m_ref == -INFINITY ? 0.f : m_ref;
       const float wr = w_ref == -INFINITY ? 0.f : w_ref;
       float sum = 0.f;
