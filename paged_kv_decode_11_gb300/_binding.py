@@ -111,8 +111,9 @@ def _load_native() -> None:
     global _native, _native_error
     try:
         from . import _native as native
-        if native.built_for != native_target():
-            raise ImportError(f"it was built for {native.built_for}, this is {native_target()}")
+        built_for = getattr(native, "built_for", "an older version")
+        if built_for != native_target():
+            raise ImportError(f"it was built for {built_for}, this is {native_target()}")
     except ImportError as e:
         _native_error = e
         return

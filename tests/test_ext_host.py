@@ -81,6 +81,14 @@ def test_a_native_module_for_another_torch_is_not_used(lib, tmp_path):
     assert "built for " + build.native_target() in out[1] and "torch 0.1" in out[1]
 
 
+def test_a_native_module_that_names_no_torch_is_not_used(lib, tmp_path):
+    before = ("import sys, types\nP._native = types.ModuleType('_native')\n"
+              "sys.modules['paged_kv_decode_11_gb300._native'] = P._native")
+    out = _elsewhere(tmp_path, OLD_CALLS.format(before=before), True)
+    assert str(P.paged_attn_decode_workspace_size(4, 8, 2, 128, 128, 64)) in out[0]
+    assert "older version" in out[1]
+
+
 def test_build_sees_that_torch_changed(lib, monkeypatch):
     assert build.up_to_date()
     monkeypatch.setattr(build, "native_target", lambda: "torch 0.1, Python 3.0, other")
