@@ -292,7 +292,9 @@ __global__ void __launch_bounds__(PrefillTcCfg<D, NST, KV == KV_E4M3, ALONE, MOD
   const int head = first - origin;                      // keys of that page no row sees
   const int P0 = ctx - L - origin;
   const int rows_used = p.q_tile * G;                   // tile rows holding (token, head) pairs
-  const int key_end = max(P0 + i1, prefix - origin);    // keys any row of the tile sees: < key_end
+  // keys any row of the tile sees: < key_end (MOD apart: the maximum with a constant 0 cost
+  // the plain kernel 0.8 % of a long chunk, 138.6 us for 137)
+  const int key_end = MOD ? max(P0 + i1, prefix - origin) : P0 + i1;
   const int n_pages = (key_end + kBS - 1) / kBS;
   const int n_tiles_all = (key_end + kTcKeys - 1) / kTcKeys;
   // this CTA's share of the key tiles: [t_begin, t_begin + n_tiles); its
