@@ -425,8 +425,9 @@ pkv_status rope_reshape_and_cache(void* query, const void* key, const void* valu
  *           query_out may be query itself (in place), or both NULL.
  *   A stored scale of 255 (NaN) counts as 254, the codes beside it as they are.
  *   A block that the call writes belongs to one sequence: copy a shared,
- *   partly filled block before appending to it. (Two sequences that write one
- *   block leave its contents undefined, nothing else.)
+ *   partly filled block before appending to it. (Two sequences, or two entries
+ *   of one's table row, through which one block is written leave its contents
+ *   undefined, nothing else.)
  *   A sequence with L_n > seq_lens[n], a context past its row of block_tables
  *   or rows outside the total_q_tokens sets PKV_DEVERR_QLEN, one with
  *   seq_lens[n] > max_position sets PKV_DEVERR_POSITION, and is skipped whole

@@ -69,7 +69,8 @@ def test_prefill_nan_scales_are_all_a_share_sees(seqs, at, which, kw):
 @pytest.mark.parametrize("seqs,at", NAN_PLACES)
 def test_prefill_nan_v_scales_leave_lse_alone(seqs, at, kw):
     # lse is a sum over scores, in which V has no part
-    for copies in (1, 12, 24, 60) if sum(seqs[0]) > 4000 else (1,):
+    many = (1, 12) if "window" in kw else (1, 12, 24, 60)
+    for copies in many if sum(seqs[0]) > 4000 else (1,):
         c = Case(204, seqs * copies, **kw)
         ref = c.want()
         for n in {0, copies - 1}:
