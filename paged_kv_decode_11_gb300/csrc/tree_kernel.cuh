@@ -69,7 +69,7 @@ struct TreeCfg {
   static constexpr int NSS = !KV8 ? 0 : D <= 128 ? 2 : 1;  // staging stages per operand
   static constexpr int STG_PAGE = kBS * D;
   static constexpr int STG_BYTES = PAGES * STG_PAGE;
-  static constexpr int SMEM_BYTES = 1024 + Q_BYTES + 2 * NST * KV_BYTES + 2 * NSS * STG_BYTES;
+  static constexpr int SMEM_BYTES = Q_BYTES + 2 * NST * KV_BYTES + 2 * NSS * STG_BYTES;
   static constexpr uint32_t TMEM_COLS = 512;
   // What a segment costs beside its tiles, in tiles, for the ranges' lengths. (0, 2, 3, 4, 6 and 8
   // tiles: 108, 66, 61, 59, 59 and 64 us on 64 contexts of 100 to 1,500 tokens; 200, 168, 163, 163,
@@ -77,7 +77,6 @@ struct TreeCfg {
   // 179, 169, 163, 165 and 170 us.)
   static constexpr int COST = 4;
   static_assert(NSB * KEYS + D <= (int)TMEM_COLS, "tensor memory");
-  static_assert(SMEM_BYTES + 2048 <= 227 * 1024, "shared memory (dynamic + static)");
 };
 
 // What a sequence asks for.
@@ -105,6 +104,28 @@ struct TreeStart {
   TreeSeq s;
   int n, h, r, t0;
   int64_t ahead;                      // key tiles of all items before it
+};
+
+// What the CTA's warps share beside the tiles, which begin at the next KB behind it.
+template <int D, bool KV8, bool QBF16>
+struct TreeShared {
+  using Cfg = TreeCfg<D, KV8>;
+  uint64_t full_k[Cfg::NST], empty_k[Cfg::NST], full_v[Cfg::NST], empty_v[Cfg::NST];
+  uint64_t s_bar[Cfg::NSB], o_bar[Cfg::NSB], p_bar[Cfg::NSB];   // S ready, P.V done, P written
+  uint64_t q_bar;                                       // a segment's queries are in place
+  TreeStart begin, end;                                 // of the range, and of the next one
+  uint32_t tmem_base;
+  // KV8, bf16 q: the shift of each row, of four segments (S runs three tiles ahead at most)
+  int8_t shift[KV8 && QBF16 ? 4 : 1][kTreeRows];
+  union {
+    int64_t sum[2][Cfg::WARPS];                         // the plan's
+    // what a row's threads tell each other: of a tile's maximum (two tiles), and at a
+    // segment's end their log2 sums
+    float top[Cfg::NG > 1 ? 2 : 1][Cfg::NG][kTreeRows];
+    float lse[Cfg::NG][kTreeRows];
+  };
+  // 16-bit: which keys of a tile with a part of the tree a softmax warp's rows see
+  uint32_t seen[KV8 ? 1 : 2][KV8 ? 1 : Cfg::KEYS / 32][4];
 };
 
 // The item and key tile at place `at` of a sequence, `ahead` key tiles behind the first one's.
@@ -270,26 +291,20 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
   using Work = TreeWork<Cfg::KEYS, KV8>;
   constexpr int NG = Cfg::NG, NST = Cfg::NST, NSB = Cfg::NSB, KEYS = Cfg::KEYS;
   constexpr int PAGES = Cfg::PAGES, NSS = KV8 ? Cfg::NSS : 1;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full_k[NST], empty_k[NST], full_v[NST], empty_v[NST];
-  __shared__ uint64_t s_bar[NSB], o_bar[NSB], p_bar[NSB];   // S ready, P written, P.V done
-  __shared__ uint64_t q_bar;                            // a segment's queries are in place
-  __shared__ uint32_t tmem_base;
-  // KV8, bf16 q: the shift of each row, of four segments (S runs three tiles ahead at most)
-  __shared__ int8_t s_shift[KV8 && QBF16 ? 4 : 1][kTreeRows];
-  // what a row's threads tell each other: of a tile's maximum (two tiles' bits, bf16), and
-  // at a segment's end their log2 sums
-  __shared__ union { uint16_t top[2][NG][kTreeRows]; float lse[NG][kTreeRows]; } s_share;
-  // 16-bit: which keys of a tile with a part of the tree a softmax warp's rows see
-  __shared__ uint32_t s_seen[KV8 ? 1 : 2][KV8 ? 1 : KEYS / 32][4];
-  __shared__ int64_t s_sum[2][Cfg::WARPS];
-  __shared__ TreeStart s_begin, s_end;                  // of the range, and of the next one
+  using Shared = TreeShared<D, KV8, QBF16>;
+  static_assert((sizeof(Shared) + 1023) / 1024 * 1024 + Cfg::SMEM_BYTES <= 227 * 1024,
+                "shared memory (static + dynamic)");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ Shared shared;
+  auto &full_k = shared.full_k, &empty_k = shared.empty_k;
+  auto &full_v = shared.full_v, &empty_v = shared.empty_v;
+  auto &s_bar = shared.s_bar, &o_bar = shared.o_bar, &p_bar = shared.p_bar;
+  auto& q_bar = shared.q_bar;
+  auto &s_begin = shared.begin, &s_end = shared.end;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* pQ = smem_raw + (base - raw);
-  uint8_t* pK = pQ + Cfg::Q_BYTES;
+  const uint32_t base = smem_u32(smem_raw);
+  uint8_t* pK = smem_raw + Cfg::Q_BYTES;
   uint8_t* pV = pK + NST * Cfg::KV_BYTES;
   uint8_t* pStg = pV + NST * Cfg::KV_BYTES;
   const uint32_t sQ = base, sK = sQ + Cfg::Q_BYTES, sV = sK + NST * Cfg::KV_BYTES;
@@ -315,7 +330,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
     mbar_init(&q_bar, KV8 ? Cfg::PK : 32 * Cfg::PK);
     fence_barrier_init();
   }
-  if (warp == 0) tc::alloc(&tmem_base, Cfg::TMEM_COLS);
+  if (warp == 0) tc::alloc(&shared.tmem_base, Cfg::TMEM_COLS);
   // the merge behind this kernel may become resident now; it waits for this grid
   if (tid == 0) griddep_launch_dependents();
   // launched as a programmatic dependent: nothing is read before the grids ahead are done
@@ -358,19 +373,19 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
     int64_t ahead_p = a - my_places, ahead_t = b - my_tiles;
     if (!alone) {
       if (lane == 31) {
-        s_sum[0][warp] = a;
-        s_sum[1][warp] = b;
+        shared.sum[0][warp] = a;
+        shared.sum[1][warp] = b;
       }
       __syncthreads();
       places = tiles = 0;
 #pragma unroll 1
       for (int w = 0; w < Cfg::WARPS; ++w) {
         if (w < warp) {
-          ahead_p += s_sum[0][w];
-          ahead_t += s_sum[1][w];
+          ahead_p += shared.sum[0][w];
+          ahead_t += shared.sum[1][w];
         }
-        places += s_sum[0][w];
-        tiles += s_sum[1][w];
+        places += shared.sum[0][w];
+        tiles += shared.sum[1][w];
       }
     }
     per = max((places + p.ctas - 1) / p.ctas, (int64_t)1);
@@ -397,7 +412,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
   const int64_t begin = cta * per;
   const int n_tiles = begin >= places ? 0 : (int)((begin + per >= places ? tiles : s_end.ahead) -
                                                   s_begin.ahead);
-  const uint32_t tm = tmem_base;
+  const uint32_t tm = shared.tmem_base;
   const uint32_t tS = tm;                               // S buffer b at KEYS b, group g's half at 64 g
   const uint32_t tO = tm + NSB * KEYS;
   // Copies of a tile's rows in the MMA's 128: the softmax's part of a tile is 64 keys for
@@ -556,7 +571,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
                            bf16x2_to_f16x2_scaled(x.z, inv), bf16x2_to_f16x2_scaled(x.w, inv));
             if (q_chunk == 0)
 #pragma unroll 1
-              for (int m = qr; m < kTreeRows; m += RP) s_shift[q_seg & 3][m] = (int8_t)sh;
+              for (int m = qr; m < kTreeRows; m += RP) shared.shift[q_seg & 3][m] = (int8_t)sh;
           }
 #pragma unroll 1
           for (int m = qr; m < kTreeRows; m += RP) sts128(dst + tree_swz(m, q_chunk % 8), x);
@@ -801,8 +816,8 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
             const uint32_t lo = __reduce_or_sync(0xFFFFFFFFu, mine ? (uint32_t)see : 0u);
             const uint32_t hi = __reduce_or_sync(0xFFFFFFFFu, mine ? (uint32_t)(see >> 32) : 0u);
             if (lane == 0) {
-              s_seen[u & 1][2 * grp][warp & 3] = lo;
-              s_seen[u & 1][2 * grp + 1][warp & 3] = hi;
+              shared.seen[u & 1][2 * grp][warp & 3] = lo;
+              shared.seen[u & 1][2 * grp + 1][warp & 3] = hi;
             }
             if constexpr (NG == 1) named_barrier(1, Cfg::SOFT);
           }
@@ -811,7 +826,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
         tc::fence_after();
         if (u == u0) {
           sl2 = p.qk_scale_log2;                        // undoes the row's q scaling
-          if constexpr (KV8 && QBF16) sl2 *= pow2f(s_shift[seg & 3][r]);
+          if constexpr (KV8 && QBF16) sl2 *= pow2f(shared.shift[seg & 3][r]);
           if constexpr (KV8 && !BSC) sl2 *= static_cast<const float*>(p.k_scales)[w.h];
           if (sl2 == 0.f) sl2 = 0x1p-126f;              // (a scale of 0: -inf stays -inf)
         }
@@ -852,13 +867,12 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
             if ((bytes & 0xFFu) == 255u && seen != 0u) l = __int_as_float(0x7FFFFFFF);
           }
         }
-        // the row's maximum over the groups, rounded up to bf16, as both its threads see it
+        // the row's maximum over the groups, as both its threads see it
         float o_top = BSC ? mxw : mx;
         if constexpr (NG > 1) {
-          s_share.top[u & 1][grp][r] = __bfloat16_as_ushort(__float2bfloat16_ru(o_top));
+          shared.top[u & 1][grp][r] = o_top;
           named_barrier(1, Cfg::SOFT);
-          o_top = fmaxf(__uint_as_float((uint32_t)s_share.top[u & 1][0][r] << 16),
-                        __uint_as_float((uint32_t)s_share.top[u & 1][1][r] << 16));
+          o_top = fmaxf(shared.top[u & 1][0][r], shared.top[u & 1][1][r]);
         }
         // O's reference moves when P would pass 2^15, then to 2^7 below the row's maximum
         float& o_ref = BSC ? w_ref : m_ref;
@@ -936,7 +950,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
           uint8_t* vtile = pV + st * Cfg::KV_BYTES;
 #pragma unroll 1
           for (int k = 0; k < KEYS / 32; ++k) {
-            const uint32_t* seen4 = s_seen[u & 1][k];
+            const uint32_t* seen4 = shared.seen[u & 1][k];
             const uint32_t some = seen4[0] | seen4[1] | seen4[2] | seen4[3];
             if (some == 0xFFFFFFFFu) continue;
 #pragma unroll 1
@@ -966,16 +980,16 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
       const bool whole = w.cnt == w.s.kt;               // else: a part, for the merge
       float lse = !(l == 0.f) ? m_ref + tree_lg2(l) : -INFINITY;
       if (NG > 1 || reps > 1) {
-        s_share.lse[grp][r] = lse;
+        shared.lse[grp][r] = lse;
         named_barrier(1, Cfg::SOFT);
         const int k0 = whole ? 0 : copy, k1 = whole ? reps : copy + 1;
         float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
         for (int i = NG * k0; i < NG * k1; ++i)
-          top = fmaxf(top, s_share.lse[i % NG][(i / NG) * RP + row]);
+          top = fmaxf(top, shared.lse[i % NG][(i / NG) * RP + row]);
 #pragma unroll 1
         for (int i = NG * k0; i < NG * k1; ++i) {
-          const float v = s_share.lse[i % NG][(i / NG) * RP + row];
+          const float v = shared.lse[i % NG][(i / NG) * RP + row];
           sum += v == -INFINITY ? 0.f : tree_ex2(v - top);
         }
         lse = !(sum == 0.f) ? top + tree_lg2(sum) : -INFINITY;
@@ -1053,7 +1067,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
           }
         }
       }
-      named_barrier(1, Cfg::SOFT);                      // s_share, the copies' space
+      named_barrier(1, Cfg::SOFT);                      // shared.lse, the copies' space
       u0 += w.cnt;
       if constexpr (KV8 && !BSC) then.next();
       w = then;
