@@ -315,11 +315,12 @@ __global__ void __launch_bounds__(32 * kKeepWarps, 5)
 }
 
 pkv_status launch_keep_path(const KeepPathParams& p, bool block_scaled, cudaStream_t stream) {
+  // (no caches: one CTA a sequence, for the new lengths)
   if (block_scaled) {
-    const int ctas = (p.num_caches * p.Hkv + kKeepWarps - 1) / kKeepWarps;
+    const int ctas = std::max(1, (p.num_caches * p.Hkv + kKeepWarps - 1) / kKeepWarps);
     return launch_dependent(keep_path_block_kernel, p, dim3(ctas, p.num_seqs), 32 * kKeepWarps, stream);
   }
-  const int64_t columns = (int64_t)p.num_caches * p.Hkv * (p.row_bytes / 16);
+  const int64_t columns = std::max<int64_t>(1, (int64_t)p.num_caches * p.Hkv * (p.row_bytes / 16));
   const dim3 grid((unsigned)((columns + kMoveThreads - 1) / kMoveThreads), p.num_seqs);
   return launch_dependent(keep_path_kernel, p, grid, kMoveThreads, stream);
 }
