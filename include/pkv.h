@@ -645,7 +645,9 @@ pkv_status kv_copy_blocks(void* const* caches, const size_t* block_bytes, int nu
  *   unused, in the order of the rows. new_tables and new_lens are other buffers than
  *   block_tables and seq_lens, which stay as they are.
  *   No block left: the entry and copies[r] are -1, PKV_DEVERR_POOL. Entries that are -1
- *   stay so; one >= num_blocks sets PKV_DEVERR_BLOCK_ID and is not counted. A length below
+ *   stay so; one >= num_blocks sets PKV_DEVERR_BLOCK_ID and is not counted. Where a parent's
+ *   partly filled block is such an entry there is nothing to copy: the rows that would get
+ *   a block of their own have -1 there, and copies[r] = (-1, -1). A length below
  *   0 or above the row's width counts as 0 (PKV_DEVERR_SEQ_LEN), a parent >= num_rows as
  *   none (PKV_DEVERR_PATH). A count that would fall below 0 stays (PKV_DEVERR_POOL).
  *   num_rows <= 16384; BS a power of two from 1 to 64. The table and counts of a pool

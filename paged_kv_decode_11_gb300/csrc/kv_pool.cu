@@ -219,6 +219,8 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
 }
 
 constexpr int kAsks = 1 << 30;                          // (in a row's parent) it gets a block of its own
+constexpr int kLacks = 1 << 30;                         // (in a row's length) its last, partly filled
+                                                        // block is none of the pool's
 constexpr int kForkBatch = 8;                           // a lane's entries whose loads are under way
 
 __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
@@ -227,36 +229,48 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   int* s_sums = s_rows;                                 // [rows + 1] rows that ask for a block; before
   int* s_first = s_rows;                                // that a row's first descendant
   int* s_parent = s_rows + p.rows + 1;                  // [rows], -1: none
-  int* s_len = s_parent + p.rows;                       // [rows] of the old table
+  int* s_len = s_parent + p.rows;                       // [rows] of the old table, kLacks with it
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
   const int warp = (int)pool_rank() * kPoolWarps + (threadIdx.x >> 5);
   unsigned int* err = warp < kPoolWarps ? p.err : nullptr;   // (one CTA reports)
+  const int part = (1 << p.bs_log2) - 1;
   for (int r = threadIdx.x; r < p.rows; r += kPoolThreads) {
     const int q = p.parents[r], len = p.lens[r];
     if (q >= p.rows && err != nullptr) atomicOr(err, PKV_DEVERR_PATH);
     s_parent[r] = q < p.rows ? max(q, -1) : -1;
     // a length that the width does not hold counts as 0
-    s_len[r] = pool_blocks(len, p.bs_log2, p.width, err) < 0 ? 0 : len;
+    const bool bad = pool_blocks(len, p.bs_log2, p.width, err) < 0;
+    // a last block that is not there (the pool had run out) cannot be copied: its row's
+    // descendants lack it too
+    bool lacks = false;
+    if (!bad && (len & part) != 0) {
+      const int last = p.tables[(int64_t)r * p.width + (len >> p.bs_log2)];
+      lacks = last < 0 || last >= p.num_blocks;
+      if (last >= p.num_blocks && err != nullptr) atomicOr(err, PKV_DEVERR_BLOCK_ID);
+    }
+    s_len[r] = bad ? 0 : lacks ? len | kLacks : len;
     s_first[r] = p.rows;
   }
   __syncthreads();
   for (int r = threadIdx.x; r < p.rows; r += kPoolThreads)
     if (s_parent[r] >= 0) atomicMin(s_first + s_parent[r], r);
   __syncthreads();
-  const int part = (1 << p.bs_log2) - 1;
   for (int r = threadIdx.x; r < p.rows; r += kPoolThreads) {
     const int q = s_parent[r];
     if (q >= 0 && (s_len[q] & part) != 0 && s_first[q] != r) s_parent[r] = q | kAsks;
   }
   __syncthreads();
   auto asks = [&](int r) { return s_parent[r] >= kAsks; };
-  pool_sums(s_sums, p.rows, [&](int r) { return asks(r) ? 1 : 0; });
+  pool_sums(s_sums, p.rows, [&](int r) {
+    return asks(r) && (s_len[s_parent[r] & ~kAsks] & kLacks) == 0 ? 1 : 0;
+  });
   for (int r = warp; r < p.rows; r += kPoolCtas * kPoolWarps) {
-    const int q = s_parent[r] < 0 ? -1 : s_parent[r] & ~kAsks, len = q >= 0 ? s_len[q] : 0;
+    const int q = s_parent[r] < 0 ? -1 : s_parent[r] & ~kAsks;
+    const int len = q >= 0 ? s_len[q] & ~kLacks : 0;
     const int mine = asks(r) ? len >> p.bs_log2 : (len + part) >> p.bs_log2;   // shared entries
-    const int held = (s_len[r] + part) >> p.bs_log2;
+    const int held = ((s_len[r] & ~kLacks) + part) >> p.bs_log2;
     const int32_t* old = p.tables + (int64_t)r * p.width;
     const int32_t* from = p.tables + (int64_t)max(q, 0) * p.width;
     int32_t* to = p.new_tables + (int64_t)r * p.width;
@@ -287,7 +301,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   // given back only when every descendant has taken its share, so that no count in use
   // passes through 0
   for (int r = warp; r < p.rows; r += kPoolCtas * kPoolWarps) {
-    const int held = (s_len[r] + part) >> p.bs_log2;
+    const int held = ((s_len[r] & ~kLacks) + part) >> p.bs_log2;
     const int32_t* old = p.tables + (int64_t)r * p.width;
     const int32_t* to = p.new_tables + (int64_t)r * p.width;
     for (int j0 = lane; j0 < held; j0 += 32 * kForkBatch) {

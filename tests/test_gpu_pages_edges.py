@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import paged_kv_decode_11_gb300 as P
-from tests.test_gpu_pages import i32, ok
+from tests.test_gpu_pages import BLOCK_ID, POOL, i32, ok
 
 pytestmark = pytest.mark.gpu
 
@@ -19,6 +19,45 @@ def _lib():
     P.load()
     torch.cuda.init()
     P.pkv_get_device_error()
+
+
+def flagged():
+    torch.cuda.synchronize()
+    return P.pkv_get_device_error()
+
+
+def fork(tables, lens, parents, refs, bs=16):
+    tables, lens, refs = i32(tables), i32(lens), i32(refs)
+    new, new_lens = torch.full_like(tables, 77), torch.full_like(lens, 77)
+    copies = torch.full((len(parents), 2), 77, dtype=torch.int32, device="cuda")
+    P.kv_fork_blocks(new, new_lens, tables, lens, i32(parents), refs, copies, bs)
+    bits = flagged()
+    return new.tolist(), new_lens.tolist(), refs.tolist(), copies.tolist(), bits
+
+
+def test_fork_of_a_row_that_lacks_its_last_block():
+    # the pool ran out when the row grew: its descendants lack the block too, and nothing is copied
+    tables, lens, refs = i32([[2, 0, -1, -1], [1, 3, -1, -1]]), [32, 20], i32([1, 1, 1, 1, 0])
+    P.kv_resize_blocks(tables, i32(lens), i32([33, 49]), refs, 16)
+    assert flagged() == POOL and tables.tolist() == [[2, 0, 4, -1], [1, 3, -1, -1]]
+    P.kv_resize_blocks(tables, i32([33, 49]), i32([0, 49]), refs, 16)
+    ok()
+    new, lens, refs, copies, bits = fork(tables.tolist(), [0, 49], [1, 1], refs.tolist())
+    assert bits == 0 and lens == [49, 49]
+    assert new == [[1, 3, -1, -1]] * 2 and refs == [0, 2, 0, 2, 0]
+    assert copies == [[-1, -1]] * 2
+    # one that has its block is copied beside it
+    new, _, refs, copies, bits = fork([[1, 3, -1, -1], [2, 4, -1, -1], [-1] * 4, [-1] * 4],
+                                      [49, 20, 0, 0], [0, 1, 0, 1], [0, 1, 1, 1, 1, 0])
+    assert bits == 0 and refs == [1, 2, 2, 2, 1, 0]
+    assert new == [[1, 3, -1, -1], [2, 4, -1, -1], [1, 3, -1, -1], [2, 0, -1, -1]]
+    assert copies == [[-1, -1], [-1, -1], [-1, -1], [4, 0]]
+
+
+def test_fork_of_a_row_whose_last_block_is_outside_the_pool():
+    new, _, refs, copies, bits = fork([[1, 9, -1], [-1] * 3], [20, 0], [0, 0], [0, 1, 0, 0])
+    assert bits == BLOCK_ID and refs == [0, 2, 0, 0]
+    assert new == [[1, 9, -1], [1, -1, -1]] and copies == [[-1, -1]] * 2
 
 
 @pytest.mark.parametrize("kv", [1, 3])                        # bf16; E4M3 with block scales
