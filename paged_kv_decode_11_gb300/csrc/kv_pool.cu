@@ -286,10 +286,9 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
       for (int k = 0; k < kForkBatch; ++k) {
         if (j0 + 32 * k >= p.width) continue;
         to[j0 + 32 * k] = next[k];
-        // (an entry that stays the same block's: one more and one less)
-        if (next[k] == was[k]) continue;
         if (next[k] >= p.num_blocks) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-        else if (next[k] >= 0) atomicAdd(p.refs + next[k], 1);
+        // (an entry that stays the same block's: one more and one less)
+        else if (next[k] >= 0 && next[k] != was[k]) atomicAdd(p.refs + next[k], 1);
       }
     }
     if (lane == 0) {

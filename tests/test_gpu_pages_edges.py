@@ -60,6 +60,13 @@ def test_fork_of_a_row_whose_last_block_is_outside_the_pool():
     assert new == [[1, 9, -1], [1, -1, -1]] and copies == [[-1, -1]] * 2
 
 
+def test_fork_flags_entries_outside_the_pool_that_stay():
+    for parents in ([0, 1], [0, -1]):
+        new, _, refs, _, bits = fork([[1, 9, 2], [0, -1, -1]], [48, 3], parents, [1, 1, 1, 0])
+        assert bits == BLOCK_ID and new[0] == [1, 9, 2]
+        assert refs == [1 if parents[1] == 1 else 0, 1, 1, 0]
+
+
 @pytest.mark.parametrize("kv", [1, 3])                        # bf16; E4M3 with block scales
 def test_lengths_of_a_path_in_no_layer(kv):
     lib = P.load()
