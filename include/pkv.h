@@ -601,7 +601,8 @@ pkv_status paged_attn_tree(void* out, const void* q, pkv_dtype q_dtype, const vo
  *   A path that does not rise, leaves its tree or is longer than max_path, or a tree
  *   that does not fit its context or the table's row, sets PKV_DEVERR_PATH: nothing of
  *   that sequence moves and new_seq_lens[n] = seq_lens[n]. A token whose source or
- *   destination block id is outside the pool sets PKV_DEVERR_BLOCK_ID and is skipped.
+ *   destination block id is outside the pool sets PKV_DEVERR_BLOCK_ID and is skipped: its
+ *   slot counts as one that no token reaches, a block of such slots alone stays as it is.
  *   Blocks from P_n on belong to one sequence. BS 1 .. 64 (block scales 16, 32, 64);
  *   D in {64, 128, 256}. One kernel for every 64 layers.
  */

@@ -8,6 +8,7 @@
 // caches 4.3; 64 paths of up to 60 in 32 block-scaled caches 17.5.
 #include <cuda_runtime.h>
 #include <algorithm>
+#include <climits>
 #include "block_scale.cuh"
 #include "launch_pages.h"
 
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(32 * kKeepWarps, 5)
       uint8_t* to = cache + dst * block_bytes;
       const int old = scales[(int64_t)dst * p.Hkv];
       uint4 v[kKeepChunks];
-      int s[kKeepChunks];                             // its scale; -1: no such chunk
+      int s[kKeepChunks];                             // its scale; -1: no such chunk or source
       auto read = [&](int q0) {
 #pragma unroll
         for (int k = 0; k < kKeepChunks; ++k) {
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(32 * kKeepWarps, 5)
                                                  (int64_t)s_slot[i] * p.row_bytes + 16 * (q % cpr));
         }
       };
-      int need = kBlockMinExp;
+      int need = INT_MIN;
       for (int q0 = 0; q0 < chunks; q0 += 32 * kKeepChunks) {
         read(q0);
 #pragma unroll
@@ -281,6 +282,8 @@ __global__ void __launch_bounds__(32 * kKeepWarps, 5)
           if (s[k] >= 0) need = max(need, chunk_exponent(v[k], s[k]));
       }
       need = __reduce_max_sync(0xFFFFFFFFu, need);    // (every row, and scale, has been read)
+      if (need == INT_MIN) continue;                  // every source's block is outside the pool
+      need = max(need, kBlockMinExp);
       const int was = min(old, 254) - kE8M0Bias, now = off == 0 ? need : max(was, need);
       for (int q0 = 0; q0 < chunks; q0 += 32 * kKeepChunks) {
         if (chunks > 32 * kKeepChunks) {
@@ -300,9 +303,10 @@ __global__ void __launch_bounds__(32 * kKeepWarps, 5)
         __syncwarp();
       }
       if (off > 0 && now != was) {
-        // the slots beside the path's, to the exponent that has grown
-        for (int q = lane; q < (bs - cnt) * cpr; q += 32) {
-          const int k = q / cpr, row = k < off ? k : k + cnt;
+        // the slots that nothing reached, to the exponent that has grown
+        for (int q = lane; q < bs * cpr; q += 32) {
+          const int row = q / cpr, k = row - off;
+          if (k >= 0 && k < cnt && s_src[first - k0 + k] >= 0) continue;
           uint4* at = reinterpret_cast<uint4*>(to + (int64_t)row * p.row_bytes + 16 * (q % cpr));
           *at = rescale16(*at, was - now);
         }

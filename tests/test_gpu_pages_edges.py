@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import paged_kv_decode_11_gb300 as P
-from tests.test_gpu_pages import BLOCK_ID, POOL, i32, ok
+from tests.test_gpu_pages import BLOCK_ID, POOL, Keep, i32, ok
 
 pytestmark = pytest.mark.gpu
 
@@ -65,6 +65,37 @@ def test_fork_flags_entries_outside_the_pool_that_stay():
         new, _, refs, _, bits = fork([[1, 9, 2], [0, -1, -1]], [48, 3], parents, [1, 1, 1, 0])
         assert bits == BLOCK_ID and new[0] == [1, 9, 2]
         assert refs == [1 if parents[1] == 1 else 0, 1, 1, 0]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "head", "block"])
+def test_paths_with_blocks_outside_the_pool(kv):
+    good = (33, 9, [2, 4])
+
+    def check(seq, bad_entry, moved):
+        # as if the path were `moved` alone, with all of its length
+        p, l, path = seq
+        for seed in (20, 21):
+            c = Keep(seed, [good, seq, good], kv=kv)
+            if kv != "bf16":                                  # what moves outgrows what it meets
+                b, o = int(c.tables[1, (p + path[1]) // 16]), (p + path[1]) % 16
+                c.caches[0].view(torch.uint8)[b, :, o] = 0x7E
+                if kv == "block":
+                    c.scales[0][b] = 150
+            c.path_lens[1] = len(moved)
+            assert path[:len(moved)] == moved
+            want = c.want()
+            want[2][1] = p + len(path)
+            c.path_lens[1] = len(path)
+            c.tables[1, bad_entry] = 10 ** 6
+            c.run()
+            assert flagged() == BLOCK_ID
+            c.check(want)
+
+    check((20, 40, [0, 14, 30]), 3, [0, 14])                   # the last one's source
+    check((20, 44, [1, 14, 30, 43]), 3, [1, 14])
+    check((32, 40, [20, 25]), 3, [])                          # every source of a fresh block
+    check((20, 40, [13, 14, 15]), 1, [])                      # the destination
+    check((30, 40, [1, 2]), 2, [1])                           # the last one's source, of larger values
 
 
 @pytest.mark.parametrize("kv", [1, 3])                        # bf16; E4M3 with block scales
