@@ -591,7 +591,8 @@ pkv_status paged_attn_tree(void* out, const void* q, pkv_dtype q_dtype, const vo
  *   paths: int32 [num_seqs, max_path], path_lens: int32 [num_seqs]: of sequence n the
  *           nodes paths[n][0 .. path_lens[n]-1], strictly rising, each < L_n. The token at
  *           position P_n + paths[n][i] moves to position P_n + i. A path of 0 moves nothing.
- *   new_seq_lens: optional int32 [num_seqs] (not seq_lens itself): P_n + path_lens[n].
+ *   new_seq_lens: optional int32 [num_seqs]: P_n + path_lens[n]. A buffer of its own: not
+ *           seq_lens, cu_q_lens, paths or path_lens.
  *   Positions behind the path keep what they had or what moved from there. Block scales: a
  *   block that gets tokens of the path gets them as rope_append_block_scaled would append
  *   their values (unrotated), its scale and the slots beside them too; the elements are
@@ -644,7 +645,7 @@ pkv_status kv_copy_blocks(void* const* caches, const size_t* block_bytes, int nu
  *   ref_counts: one more for each new entry, one less for each entry of block_tables, so
  *   that blocks no new row names become unused; new blocks are the lowest that are then
  *   unused, in the order of the rows. new_tables and new_lens are other buffers than
- *   block_tables and seq_lens, which stay as they are.
+ *   block_tables, seq_lens and parents, which stay as they are.
  *   No block left: the entry and copies[r] are -1, PKV_DEVERR_POOL. Entries that are -1
  *   stay so; one >= num_blocks sets PKV_DEVERR_BLOCK_ID and is not counted. Where a parent's
  *   partly filled block is such an entry there is nothing to copy: the rows that would get

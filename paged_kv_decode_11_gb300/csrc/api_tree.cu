@@ -140,8 +140,9 @@ pkv_status kv_keep_path(void* const* k_caches, void* const* v_caches, pkv_dtype 
     return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0 || (num_layers == 0 && new_seq_lens == nullptr)) return PKV_OK;
   if (!block_tables || !seq_lens || !cu_q_lens || !path_lens || (max_path > 0 && !paths) ||
-      new_seq_lens == seq_lens)
-    return PKV_ERR_INVALID_ARG;
+      (new_seq_lens != nullptr && (new_seq_lens == seq_lens || new_seq_lens == cu_q_lens ||
+                                   new_seq_lens == paths || new_seq_lens == path_lens)))
+    return PKV_ERR_INVALID_ARG;             // (one CTA would write what another has to read)
   if (num_layers > 0 && (!k_caches || !v_caches || (block_scaled && (!k_scales || !v_scales))))
     return PKV_ERR_INVALID_ARG;
   for (int c = 0; c < num_layers; ++c) {
@@ -195,7 +196,8 @@ pkv_status kv_fork_blocks(int32_t* new_tables, int32_t* new_lens, const int32_t*
     return PKV_ERR_INVALID_ARG;
   if (num_rows == 0) return PKV_OK;
   if (!new_tables || !new_lens || !block_tables || !seq_lens || !parents || !ref_counts ||
-      !copies || new_tables == block_tables || new_lens == seq_lens || !aligned16(copies))
+      !copies || new_tables == block_tables || new_lens == seq_lens || new_lens == parents ||
+      !aligned16(copies))
     return PKV_ERR_INVALID_ARG;
   unsigned int* err = err_word();
   if (err == nullptr) return PKV_ERR_CUDA;
