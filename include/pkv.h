@@ -652,8 +652,11 @@ pkv_status kv_copy_blocks(void* const* caches, const size_t* block_bytes, int nu
  *   a block of their own have -1 there, and copies[r] = (-1, -1). A length below
  *   0 or above the row's width counts as 0 (PKV_DEVERR_SEQ_LEN), a parent >= num_rows as
  *   none (PKV_DEVERR_PATH). A count that would fall below 0 stays (PKV_DEVERR_POOL).
- *   num_rows <= 16384; BS a power of two from 1 to 64. The table and counts of a pool
- *   belong to one call at a time.
+ *   A partly filled last block of block_tables belongs to its row alone: the first new row
+ *   of a parent goes on writing into it, whatever its count. (A fork leaves its rows so;
+ *   see kv_resize_blocks for a row that is cut.)
+ *   copies: 16-byte aligned. num_rows <= 16384; BS a power of two from 1 to 64. The table
+ *   and counts of a pool belong to one call at a time.
  */
 pkv_status kv_fork_blocks(int32_t* new_tables, int32_t* new_lens, const int32_t* block_tables,
                           const int32_t* seq_lens, const int32_t* parents, int32_t* ref_counts,
@@ -671,6 +674,11 @@ pkv_status kv_fork_blocks(int32_t* new_tables, int32_t* new_lens, const int32_t*
  *   No block left: the entry is -1, PKV_DEVERR_POOL. A row with a length below 0 or above
  *   its width is left as it is (PKV_DEVERR_SEQ_LEN). Entries, counts and sizes otherwise
  *   as for kv_fork_blocks.
+ *   A row that is cut to end inside a block keeps that block, also where other rows share
+ *   it (a count above 1): it may be read so, but what the row appended next would overwrite
+ *   the others' tokens. For a block of its own cut the row to the block's beginning, then
+ *   resize it to the length, and copy: pairs (the entry before, the entry after) for
+ *   kv_copy_blocks.
  */
 pkv_status kv_resize_blocks(int32_t* block_tables, const int32_t* seq_lens,
                             const int32_t* new_lens, int32_t* ref_counts, int num_rows,

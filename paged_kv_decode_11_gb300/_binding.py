@@ -527,7 +527,9 @@ def kv_fork_blocks(new_tables: torch.Tensor, new_lens: torch.Tensor, block_table
     """new_tables[r] <- the blocks of row parents[r] of block_tables, shared (none for a negative
     parent), with a fresh block for the partly filled last one of every descendant but a row's
     first: copies[r] = (source, destination) for kv_copy_blocks, else (-1, -1). ref_counts
-    int32 [num_blocks] follow; blocks that no row names any more become unused."""
+    int32 [num_blocks] follow; blocks that no row names any more become unused. A partly filled last
+    block has to be its row's alone (kv_resize_blocks says when one is not). copies is 16-byte
+    aligned."""
     native = _native or _marshal()
     st = native.fork_blocks(new_tables, new_lens, block_tables, seq_lens, parents, ref_counts,
                             copies, block_size, _handle(stream))
@@ -538,7 +540,8 @@ def kv_resize_blocks(block_tables: torch.Tensor, seq_lens: torch.Tensor, new_len
                      ref_counts: torch.Tensor, block_size: int, stream=None) -> None:
     """Give each row of block_tables, which holds the blocks of seq_lens[r] tokens, those of
     new_lens[r]: unused blocks (ref_counts 0), lowest first, or -1 in place of those it gives
-    back."""
+    back. A row cut to end inside a block that other rows share must not write there: cut it to
+    the block's beginning, resize it to the length and copy (old entry, new entry) instead."""
     native = _native or _marshal()
     st = native.resize_blocks(block_tables, seq_lens, new_lens, ref_counts, block_size,
                               _handle(stream))

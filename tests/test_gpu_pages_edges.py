@@ -110,3 +110,30 @@ def test_lengths_of_a_path_in_no_layer(kv):
     assert st == 0
     ok()
     assert new.tolist() == [16, 6]
+
+
+def test_a_row_cut_into_a_block_that_it_shares():
+    # two samples of a prompt of 40; the second goes back to 20 tokens, into a block that is the
+    # first one's too: its own copy of that block comes of giving the block back, taking another
+    # and copying
+    bs, nb = 16, 12
+    g = torch.Generator("cuda").manual_seed(1)
+    k = torch.randn(nb, 2, bs, 64, generator=g, device="cuda").half()
+    tables, lens, refs = i32([[5, 7, 2, -1], [-1] * 4]), i32([40, 0]), i32([0, 0, 1, 0, 0, 1, 0, 1] + [0] * 4)
+    new, new_lens, copies = torch.empty_like(tables), torch.empty_like(lens), i32([[0, 0]] * 2)
+    P.kv_fork_blocks(new, new_lens, tables, lens, i32([0, 0]), refs, copies, bs)
+    P.kv_copy_blocks(k, copies)
+    ok()
+    assert new.tolist() == [[5, 7, 2, -1], [5, 7, 0, -1]]
+    want = [k[b].clone() for b in (5, 7, 2)]
+    before = new.clone()
+    P.kv_resize_blocks(new, new_lens, i32([40, 16]), refs, bs)
+    P.kv_resize_blocks(new, i32([40, 16]), i32([40, 20]), refs, bs)
+    P.kv_copy_blocks(k, torch.stack([before[:, 1], new[:, 1]], 1).contiguous())
+    ok()
+    assert new.tolist() == [[5, 7, 2, -1], [5, 0, -1, -1]]
+    assert refs.tolist() == [1, 0, 1, 0, 0, 2, 0, 1, 0, 0, 0, 0]
+    assert torch.equal(k[0], want[1])
+    k[int(new[1, 1]), :, 4:] = 9                              # what the second row writes next
+    for b, w in zip((5, 7, 2), want):
+        assert torch.equal(k[b], w)
