@@ -554,11 +554,10 @@ size_t paged_attn_tree_workspace_size(int num_q_heads, int num_kv_heads, int hea
  *   by the nodes' depths first.
  *   A row that sees nothing gives out = 0 and lse = -inf. L_n = 0 is fine; rows outside
  *   every sequence are left alone. out is not q, nor overlaps it. out_lse: optional fp32 [total_q_tokens, Hq].
- *   Keys and values that no node of a row's tile (the 128 / G nodes from a multiple of
- *   that on) sees may be NaN or anything else. A NaN or an infinity in V may reach every
- *   row of a tile in which one row sees its key, and comes out as NaN or infinity. A NaN
- *   score (from q, K or a K scale of 255) makes the row's out and lse NaN, a V scale of
- *   255 on a block that the row sees its out.
+ *   What a row does not see does not reach it, whatever it is. A NaN or an infinity in an
+ *   element of V comes out in that element of the rows that see its key (an infinity from
+ *   before the tree perhaps as NaN). A score of NaN or +infinity (from q, K or a K scale of
+ *   255) makes the row's out and lse NaN, a V scale of 255 on a block that the row sees its out.
  *   workspace: 256-byte aligned, paged_attn_tree_workspace_size() bytes, with any
  *   contents; two calls that share one must not overlap on the GPU, in no other way do
  *   they depend on each other.

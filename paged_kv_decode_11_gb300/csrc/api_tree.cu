@@ -72,6 +72,8 @@ pkv_status paged_attn_tree(void* out, const void* q, pkv_dtype q_dtype, const vo
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = p.part_o + (size_t)ctas * kTreeParts * tree_part_floats(head_dim);
   p.splits = reinterpret_cast<TreeSplit*>(p.part_lse + (size_t)ctas * kTreeParts * kTreeRows);
+  p.odd = reinterpret_cast<TreeOdd*>(p.splits + ctas + 1);
+  p.kv_dtype = kv_dtype;
   p.num_seqs = num_seqs;
   p.Hq = num_q_heads;
   p.Hkv = num_kv_heads;

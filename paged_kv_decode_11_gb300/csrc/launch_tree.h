@@ -8,6 +8,20 @@ namespace pkv {
 
 constexpr int kTreeRows = 128;        // (node, head) rows of a tile, the M of its MMAs
 constexpr int kTreeParts = 3;         // partial results of a CTA
+constexpr int tree_keys(int head_dim) { return head_dim <= 128 ? 128 : 64; }   // of a tile
+
+// What a sequence asks for.
+struct TreeSeq {
+  int q0, L, ctx;                     // first row, nodes, tokens with them
+  int kt, rt;                         // key tiles, row tiles; 0 where there is nothing to do
+};
+
+// Where a CTA's range begins: a key tile of an item.
+struct TreeStart {
+  TreeSeq s;
+  int n, h, r, t0;
+  int64_t ahead;                      // key tiles of all items before it
+};
 
 // What a CTA leaves for the merge: where its range of key tiles begins inside an
 // item (a row tile of one sequence and KV head), that item and the CTAs that share it.
@@ -16,7 +30,15 @@ struct TreeSplit {
   int row;                            // first row of q and out
   int nodes;                          // nodes of the row tile
   int head;                           // KV head
-  int pad[3];
+  int seq, node0;                     // its sequence, and of that the tile's first node
+  int pad;
+};
+
+// And where V of a tree in its range held what is no number: its range. The attention takes
+// such elements for 0; the merge adds them to the outputs of the rows that see them.
+struct TreeOdd {
+  int tiles;                          // 0: nothing of the kind
+  TreeStart begin;
 };
 
 struct TreeParams {
@@ -36,10 +58,12 @@ struct TreeParams {
   // Of CTA c: partial results 3 c (of an item that an earlier CTA began) and 3 c + 1 (of
   // one that goes on in the next), each the rows' normalised O, [D / 4][128] float4, and
   // their log2 sums [128], of every copy of a row; 3 c + 2: where the copies of a whole
-  // item are added up. Then the CTAs' TreeSplit.
+  // item are added up. Then the CTAs' TreeSplit and TreeOdd.
   float* part_o;
   float* part_lse;
   TreeSplit* splits;
+  TreeOdd* odd;
+  pkv_dtype kv_dtype;
   int num_seqs, Hq, Hkv, G, max_blocks, num_blocks, q_rows, mask_words;
   int q_tile;                         // nodes of a row tile
   int ppb_shift;                      // log2(block_size / 16)
@@ -47,11 +71,11 @@ struct TreeParams {
   float qk_scale_log2;
 };
 
-// Workspace: ctas * (three partial results, a TreeSplit).
+// Workspace: ctas * (three partial results, a TreeSplit, a TreeOdd), and a TreeSplit that is empty.
 constexpr size_t tree_part_floats(int head_dim) { return (size_t)kTreeRows * head_dim; }
 constexpr size_t tree_workspace_bytes(int ctas, int head_dim) {
   return (size_t)ctas * (kTreeParts * (tree_part_floats(head_dim) + kTreeRows) * sizeof(float) +
-                         sizeof(TreeSplit));
+                         sizeof(TreeSplit) + sizeof(TreeOdd)) + sizeof(TreeSplit);
 }
 
 // Validate nothing (the entry point does); PKV_ERR_CUDA on a launch failure. A call is two

@@ -32,6 +32,9 @@
 //   Block scales: a code stands for code * 2^e of its block and KV head; the codes go
 // through the MMAs as they are, 2^ek joins a score as a factor and P carries 2^ev as an
 // addend of its exponent, with a reference of its own for P and O.
+//   Scores that a row does not see are -inf before anything is done with them. A weight of 0
+// does not mask V (0 times NaN), so V of the tree goes into the product with 0 in place of what
+// is no number; the merge adds that to the rows that see it.
 //
 // What bounds it (GB300, 32 query heads on 8 KV heads of 128): 16-bit caches, the bandwidth:
 // another tile costs an SM 1.5 us, 6.6 TB/s over all; eight contexts of 16,384 with trees of 16
@@ -43,9 +46,8 @@
 // one another (17 with an 8-bit cache), and a segment 3 us and more.
 #pragma once
 #include "block_scale.cuh"
-#include "common.cuh"
-#include "launch_tree.h"
 #include "tc.cuh"
+#include "tree_work.cuh"
 
 namespace pkv {
 
@@ -53,7 +55,7 @@ template <int D, bool KV8>
 struct TreeCfg {
   static constexpr int NG = D <= 128 ? 2 : 1;              // softmax groups
   static constexpr int HALF = 64;                          // keys of a tile that a group takes
-  static constexpr int KEYS = NG * HALF;                   // keys per tile
+  static constexpr int KEYS = tree_keys(D);                // keys per tile
   static constexpr int PAGES = KEYS / kBS;
   static constexpr int NSB = 3;                            // S buffers
   static constexpr int PK = 4, PV = 3;                     // producer warps of K and of V
@@ -76,34 +78,8 @@ struct TreeCfg {
   // 166 and 167 us on 64 of 1,024 to 8,192; with block scales 123, 81, 74, 71, 74 and 79 us and 210,
   // 179, 169, 163, 165 and 170 us.)
   static constexpr int COST = 4;
+  static_assert(KEYS == NG * HALF, "a half of a tile to each group");
   static_assert(NSB * KEYS + D <= (int)TMEM_COLS, "tensor memory");
-};
-
-// What a sequence asks for.
-struct TreeSeq {
-  int q0, L, ctx;                     // first row, nodes, tokens with them
-  int kt, rt;                         // key tiles, row tiles; 0 where there is nothing to do
-};
-
-template <int KEYS>
-__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int q0, int q1, int ctx,
-                                            bool* bad = nullptr) {
-  TreeSeq s{q0, q1 - q0, ctx, 0, 0};
-  const bool refused = s.L < 0 || s.L > ctx || q0 < 0 || q0 > p.q_rows - s.L ||
-                       ctx > ((p.max_blocks * kBS) << p.ppb_shift) ||
-                       (p.masks != nullptr && s.L > 32 * (int64_t)p.mask_words);
-  if (bad != nullptr) *bad = refused;
-  if (refused || s.L == 0) return s;
-  s.kt = (ctx + KEYS - 1) / KEYS;
-  s.rt = (s.L + p.q_tile - 1) / p.q_tile;
-  return s;
-}
-
-// Where a CTA's range begins: a key tile of an item.
-struct TreeStart {
-  TreeSeq s;
-  int n, h, r, t0;
-  int64_t ahead;                      // key tiles of all items before it
 };
 
 // What the CTA's warps share beside the tiles, which begin at the next KB behind it.
@@ -124,8 +100,7 @@ struct TreeShared {
     float top[Cfg::NG > 1 ? 2 : 1][Cfg::NG][kTreeRows];
     float lse[Cfg::NG][kTreeRows];
   };
-  // 16-bit: which keys of a tile with a part of the tree a softmax warp's rows see
-  uint32_t seen[KV8 ? 1 : 2][KV8 ? 1 : Cfg::KEYS / 32][4];
+  uint32_t odd_v;                     // not 0: V of some tree has had elements that are no numbers
 };
 
 // The item and key tile at place `at` of a sequence, `ahead` key tiles behind the first one's.
@@ -146,108 +121,30 @@ __device__ __forceinline__ TreeStart tree_start(const TreeSeq& s, int n, int64_t
   return b;
 }
 
-// A CTA's range of key tiles as its warps walk through it, segment by segment.
-template <int KEYS, bool OUT_OF_LINE>
-struct TreeWork {
-  const TreeParams* p;
-  int left;                           // key tiles of the range behind this segment
-  TreeSeq s;                          // this segment's sequence
-  int n, h, r;                        // sequence, KV head, row tile
-  int t0, cnt;                        // key tiles [t0, t0 + cnt) of the item; cnt = 0: done
-  int nq0, nq1, nctx;                 // as they stand in memory: sequence n + 1
+// Copies of a tile's rows in the MMA's 128: the softmax's part of a tile is 64 keys for each
+// thread, 32 or 16.
+__device__ __forceinline__ int tree_copies(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
 
-  __device__ __forceinline__ void peek() {
-    nq0 = nq1 = nctx = 0;
-    if (n + 1 < p->num_seqs) {
-      nq0 = p->cu_q_lens[n + 1];
-      nq1 = p->cu_q_lens[n + 2];
-      nctx = p->seq_lens[n + 1];
-    }
-  }
-  __device__ __forceinline__ void take() {
-    cnt = min(s.kt - t0, left);
-    left -= cnt;
-  }
-  // The range of `total` key tiles that begins with key tile `start.t0` of an item.
-  __device__ __forceinline__ TreeWork(const TreeParams& params, const TreeStart& start, int total)
-      : p(&params), left(total), s(start.s), n(start.n), h(start.h), r(start.r), t0(start.t0),
-        cnt(0) {
-    if (total <= 0) return;
-    peek();
-    take();
-  }
-  __device__ __forceinline__ void step() {
-    if (left <= 0) {
-      cnt = 0;
-      return;
-    }
-    t0 = 0;
-    if (++r == s.rt) {
-      r = 0;
-      if (++h == p->Hkv) {
-        h = 0;
-        do {
-          s = tree_seq<KEYS>(*p, nq0, nq1, nctx);
-          ++n;
-          peek();
-        } while (s.rt == 0 && n < p->num_seqs);
-      }
-    }
-    take();
-  }
-  __device__ __noinline__ static TreeWork stepped(TreeWork w) {
-    w.step();
-    return w;
-  }
-  // The next segment. Six places take it, in 3 KB of code each: with an E4M3 cache, whose
-  // producers have more code than a copy, out of line (379 us on four contexts of 80,000 of 8
-  // bits, so 366; a small tree over 16 bits 13.2 us, so 13.7).
-  __device__ __forceinline__ void next() {
-    if constexpr (OUT_OF_LINE) *this = stepped(*this);
-    else step();
-  }
-  // Keys of the sequence before its tree, this item's first node and its nodes.
-  __device__ __forceinline__ int before() const { return s.ctx - s.L; }
-  __device__ __forceinline__ int node0() const { return r * p->q_tile; }
-  __device__ __forceinline__ int nodes() const { return min(p->q_tile, s.L - node0()); }
-};
-
-// Which of the 64 keys from place m0 of a tree on a node sees (m0 may be negative: keys
-// before the tree, which every row sees). node: its row of q; i: its place in the tree.
-__device__ __forceinline__ uint64_t tree_sees(const TreeParams& p, int node, int i, int m0, int L) {
-  if (m0 <= -64) return ~(uint64_t)0;
-  if (p.masks == nullptr) {
-    const int last = i - m0;          // the last one seen
-    return last < 0 ? 0u : last >= 63 ? ~(uint64_t)0 : ((uint64_t)2 << last) - 1;
-  }
-  const uint32_t* row = p.masks + (int64_t)node * p.mask_words;
-  auto word = [&](int k) { return k >= 0 && k < p.mask_words ? row[k] : 0u; };
-  const int k = m0 >> 5, s = m0 & 31;
-  const uint32_t a = word(k), b = word(k + 1), c = word(k + 2);
-  uint64_t w = ((uint64_t)__funnelshift_r(b, c, s) << 32) | __funnelshift_r(a, b, s);
-  const int end = L - m0;             // nodes behind the last
-  if (end < 64) w &= end <= 0 ? 0u : ((uint64_t)1 << end) - 1;
-  return m0 < 0 ? w | (((uint64_t)1 << -m0) - 1) : w;
+// Elements of eight 16-bit values that are no numbers (exponent all ones) to 0. True: there were
+// some.
+template <bool BF16>
+__device__ __forceinline__ bool tree_only_numbers(uint4& v) {
+  constexpr uint32_t EXP = BF16 ? 0x7F807F80u : 0x7C007C00u, ONE = BF16 ? 0x00800080u : 0x04000400u;
+  auto odd = [](uint32_t w) { return ((w & EXP) + ONE) & 0x80008000u; };   // of each, the sign bit
+  const uint32_t a = odd(v.x), b = odd(v.y), c = odd(v.z), d = odd(v.w);
+  if ((a | b | c | d) == 0u) return false;
+  auto clear = [](uint32_t w, uint32_t o) { return w & ~((o >> 15) * 0xFFFFu); };
+  v = make_uint4(clear(v.x, a), clear(v.y, b), clear(v.z, c), clear(v.w, d));
+  return true;
 }
 
-// The same for all nodes of a row tile together and KEYS keys: 1 where one of them sees the
-// key. Whole warp, each lane a part of the nodes.
-template <int KEYS>
-__device__ __forceinline__ void tree_any_sees(const TreeParams& p, int row0, int node0, int nodes,
-                                              int m0, int L, int lane, uint32_t* seen) {
-#pragma unroll
-  for (int k = 0; k < KEYS / 32; ++k) seen[k] = 0u;
-#pragma unroll 1
-  for (int i = lane; i < nodes; i += 32) {
-#pragma unroll
-    for (int k = 0; k < KEYS / 64; ++k) {
-      const uint64_t w = tree_sees(p, row0 + i, node0 + i, m0 + 64 * k, L);
-      seen[2 * k] |= (uint32_t)w;
-      seen[2 * k + 1] |= (uint32_t)(w >> 32);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < KEYS / 32; ++k) seen[k] = __reduce_or_sync(0xFFFFFFFFu, seen[k]);
+// The same for sixteen E4M3 codes (NaN is all that is no number).
+__device__ __forceinline__ bool tree_only_numbers_e4m3(uint4& v) {
+  auto odd = [](uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); };
+  const uint32_t a = odd(v.x), b = odd(v.y), c = odd(v.z), d = odd(v.w);
+  if ((a | b | c | d) == 0u) return false;
+  v = make_uint4(v.x & ~a, v.y & ~b, v.z & ~c, v.w & ~d);
+  return true;
 }
 
 __device__ __forceinline__ uint32_t tree_swz(uint32_t r, uint32_t chunk) {
@@ -267,6 +164,26 @@ __device__ __forceinline__ float tree_lg2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// A lane's chunks of a staged page of codes (of each pass one, from address `at` and tile row `row`
+// on): rows from `valid` on, which may be of a page not loaded, to 0, NaN in rows from `tree` on
+// too. True: there was such a NaN.
+template <int D>
+static __device__ __noinline__ bool tree_clean_page(uint32_t at, int row, int valid, int tree) {
+  bool odd = false;
+#pragma unroll
+  for (int k = 0; k < kBS * D / 512; ++k, at += 512, row += 512 / D) {
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (row < valid) {
+      if (row < tree) continue;
+      x = lds128(at);
+      if (!tree_only_numbers_e4m3(x)) continue;
+      odd = true;
+    }
+    sts128(at, x);
+  }
+  return odd;
 }
 
 // The rest of a bounded wait: false once it ran out. (Out of line, as what else is not on the
@@ -328,6 +245,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
       mbar_init(&p_bar[b], Cfg::SOFT / 32);
     }
     mbar_init(&q_bar, KV8 ? Cfg::PK : 32 * Cfg::PK);
+    shared.odd_v = 0u;
     fence_barrier_init();
   }
   if (warp == 0) tc::alloc(&shared.tmem_base, Cfg::TMEM_COLS);
@@ -415,9 +333,6 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
   const uint32_t tm = shared.tmem_base;
   const uint32_t tS = tm;                               // S buffer b at KEYS b, group g's half at 64 g
   const uint32_t tO = tm + NSB * KEYS;
-  // Copies of a tile's rows in the MMA's 128: the softmax's part of a tile is 64 keys for
-  // each thread, 32 or 16.
-  auto copies_of = [](int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; };
 
   const bool k_warp = warp >= Cfg::W_K && warp < Cfg::W_K + Cfg::PK;
   if (k_warp || warp >= Cfg::W_V) {
@@ -438,8 +353,11 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
         d.row = b.s.q0 + b.r * p.q_tile;
         d.nodes = min(p.q_tile, b.s.L - b.r * p.q_tile);
         d.head = b.h;
+        d.seq = b.n;
+        d.node0 = b.r * p.q_tile;
       }
       p.splits[cta] = d;
+      if (cta + 1 == p.ctas) p.splits[p.ctas] = TreeSplit{};
     }
     __syncwarp();
     const int np = k_warp ? Cfg::PK : Cfg::PV, pw = k_warp ? warp - Cfg::W_K : warp - Cfg::W_V;
@@ -541,7 +459,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
     const int q_row0 = (tid - 32 * Cfg::W_K) / CPR, q_chunk = (tid - 32 * Cfg::W_K) % CPR;
     const uint32_t inv_G = 65536u / p.G + 1u;           // x / G = x inv_G >> 16 for x < 128, G <= 16
     auto bring_queries = [&]() {
-      const int used = qw.nodes() * p.G, reps = copies_of(used), RP = kTreeRows / reps;
+      const int used = qw.nodes() * p.G, reps = tree_copies(used), RP = kTreeRows / reps;
       const uint16_t* src = static_cast<const uint16_t*>(p.q) + 8 * q_chunk +
                             ((int64_t)(qw.s.q0 + qw.node0()) * p.Hq + (int64_t)qw.h * p.G) * D;
       const uint32_t dst = sQ + (q_chunk / 8) * Cfg::Q_BOX;
@@ -599,8 +517,8 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
     } else {
       Work w(p, s_begin, n_tiles);
       int t = w.t0;
-      // the warp turns its pages of staged tile u into f16 in ring stage u % NST, rows of V
-      // that nobody sees into zeros, and refills the staging stage. A lane has the chunk of every
+      // the warp turns its pages of staged tile u into f16 in ring stage u % NST, NaN in the V of
+      // the tree into zeros, and refills the staging stage. A lane has the chunk of every
       // RP8-th row that it has copied
       uint32_t into[PASSES];
 #pragma unroll
@@ -612,36 +530,17 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
         if (u >= 0) stage_free(u);
         if (u >= 0 && u < n_tiles) {
           const int st = u % NST, valid = w.s.ctx - t * KEYS;
-          const bool tail = (t + 1) * KEYS > (k_warp ? w.s.ctx : w.before());
-          uint32_t seen[KEYS / 32];
-          if (tail) {
-            if (k_warp) {
-#pragma unroll
-              for (int k = 0; k < KEYS / 32; ++k) seen[k] = 0xFFFFFFFFu;
-            } else {
-              tree_any_sees<KEYS>(p, w.s.q0 + w.node0(), w.node0(), w.nodes(), t * KEYS - w.before(),
-                                  w.s.L, lane, seen);
-            }
-          }
+          // V: the tile's first row of the tree, where NaN has to go (of K, scores are masked)
+          const int tree = k_warp ? KEYS : w.before() - t * KEYS;
           const uint32_t src = stage + (u % NSS) * Cfg::STG_BYTES;
           const uint32_t dst = ring + st * Cfg::KV_BYTES;
 #pragma unroll 1
           for (int pg = pw; pg < PAGES; pg += np) {
+            if ((pg + 1) * kBS > tree && tree_clean_page<D>(src + pg * Cfg::STG_PAGE, pg * kBS + rsub, valid, tree))
+              shared.odd_v = 1u;
             uint4 e[PASSES];
 #pragma unroll
             for (int k = 0; k < PASSES; ++k) e[k] = lds128(src + pg * Cfg::STG_PAGE + k * 512);
-            if (tail) {
-              // rows of pages not loaded hold stale bytes; rows of V that nobody sees, anything
-              uint32_t some = 0xFFFFFFFFu;
-#pragma unroll
-              for (int k = 0; k < KEYS / 32; ++k)
-                if (pg / 2 == k) some = seen[k] >> (kBS * (pg & 1));
-#pragma unroll
-              for (int k = 0; k < PASSES; ++k) {
-                const int row = k * RP8 + rsub;
-                if (pg * kBS + row >= valid || !((some >> row) & 1u)) e[k] = make_uint4(0u, 0u, 0u, 0u);
-              }
-            }
 #pragma unroll
             for (int k = 0; k < PASSES; ++k) {
               const uint32_t to = dst + pg * (kBS * 128) + into[k];
@@ -786,7 +685,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
     if (BSC && w.cnt > 0) first_bytes(w);
     for (int u0 = 0; w.cnt > 0; ++seg) {
       const int used = w.nodes() * p.G;                 // rows of the tile
-      const int reps = copies_of(used);                 // copies of them in the 128 rows
+      const int reps = tree_copies(used);                 // copies of them in the 128 rows
       const int RP = kTreeRows / reps, copy = r / RP, row = r % RP;
       const bool mine = row < used;
       const int node = w.node0() + row / p.G;           // (of a row that is none: unused)
@@ -812,14 +711,27 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
         if (tail) {
           see = tree_sees(p, mine ? q_row : w.s.q0, mine ? node : 0,
                           t * KEYS + Cfg::HALF * grp - P, w.s.L);
-          if constexpr (!KV8) {                         // a warp's rows together
-            const uint32_t lo = __reduce_or_sync(0xFFFFFFFFu, mine ? (uint32_t)see : 0u);
-            const uint32_t hi = __reduce_or_sync(0xFFFFFFFFu, mine ? (uint32_t)(see >> 32) : 0u);
-            if (lane == 0) {
-              shared.seen[u & 1][2 * grp][warp & 3] = lo;
-              shared.seen[u & 1][2 * grp + 1][warp & 3] = hi;
+          if constexpr (!KV8) {
+            // V of the tree and of what lies behind it: zeros for what is no number, as a weight
+            // of 0 does not keep it from a row (the rows that see it get it at the end)
+            const int st = u % NST, from = max(P - t * KEYS, 0);
+            wait(&full_v[st], (u / NST) & 1);
+#pragma unroll 1
+            for (int i = tid; i < (KEYS - from) * Cfg::NBOX * 8; i += Cfg::SOFT) {
+              const int vr = from + i / (Cfg::NBOX * 8), rest = i % (Cfg::NBOX * 8);
+              uint4* at = reinterpret_cast<uint4*>(
+                  pV + st * Cfg::KV_BYTES + (rest / 8) * Cfg::KV_BOX + vr * 128 + (rest % 8) * 16);
+              if (t * KEYS + vr >= w.s.ctx) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                uint4 x = *at;
+                if (tree_only_numbers<BF16>(x)) {
+                  *at = x;
+                  shared.odd_v = 1u;
+                }
+              }
             }
-            if constexpr (NG == 1) named_barrier(1, Cfg::SOFT);
+            fence_proxy_async_smem();
           }
         }
         wait(&s_bar[b], (u / NSB) & 1);
@@ -942,27 +854,6 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
             if (i < c0 || i >= c1) tc::st8(half + 8 * i, zero);
         }
         tc::wait_st();
-        // V rows that no row of the tile sees (behind the context, or nodes outside every
-        // mask) meet weight 0: zeros, so that what they hold cannot make NaN of it
-        if (!KV8 && tail) {
-          const int st = u % NST;
-          wait(&full_v[st], (u / NST) & 1);
-          uint8_t* vtile = pV + st * Cfg::KV_BYTES;
-#pragma unroll 1
-          for (int k = 0; k < KEYS / 32; ++k) {
-            const uint32_t* seen4 = shared.seen[u & 1][k];
-            const uint32_t some = seen4[0] | seen4[1] | seen4[2] | seen4[3];
-            if (some == 0xFFFFFFFFu) continue;
-#pragma unroll 1
-            for (int i = tid; i < 32 * Cfg::NBOX * 8; i += Cfg::SOFT) {
-              const int vr = i / (Cfg::NBOX * 8), rest = i % (Cfg::NBOX * 8);
-              if (!((some >> vr) & 1u))
-                *reinterpret_cast<uint4*>(vtile + (rest / 8) * Cfg::KV_BOX + (32 * k + vr) * 128 +
-                                          (rest % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
-          fence_proxy_async_smem();
-        }
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_bar[b]);
@@ -1076,6 +967,12 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
   tc::fence_before();
   __syncthreads();
   if (warp == 0) tc::dealloc(tm, Cfg::TMEM_COLS);
+  // for the merge: V that was no number, and this range to find the rows that see it
+  if (tid == Cfg::THREADS - 1) {
+    TreeOdd* odd = p.odd + cta;
+    odd->tiles = shared.odd_v != 0u ? n_tiles : 0;
+    if (shared.odd_v != 0u) odd->begin = s_begin;
+  }
 }
 
 // One instance and its launch, as a programmatic dependent of the kernel ahead.

@@ -4,6 +4,8 @@ import pytest
 import torch
 
 import paged_kv_decode_11_gb300 as P
+from tests import ext_ref as R
+from tests import tree_ref as T
 from tests.test_gpu_tree import Case, ok
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +47,77 @@ def test_large_scores_that_lie_close_together(kw, sign, log2_score):
     got = c.run()
     ok()
     c.check(got)
+
+
+def sees(c, n, m):
+    """Of sequence n's rows (of q), those that see its node m (below 0: its context)."""
+    lo, hi = c.cu[n:n + 2].tolist()
+    i = torch.arange(hi - lo)
+    mine = (m <= i) if c.masks is None or m < 0 else c.masks[lo:hi, m]
+    rows = torch.zeros(c.q.shape[0], dtype=torch.bool)
+    rows[lo:hi] = mine
+    return rows.cuda()
+
+
+@pytest.mark.parametrize("masks", ["tree", "chain", "random"])
+@pytest.mark.parametrize("kw", [dict(kv="same"), dict(kv="same", dtype="f16", d=64), dict(kv="same", d=256),
+                                dict(kv="same", hq=32), dict(kv="same", dtype="f16", hq=32, bs=64),
+                                dict(kv="head"), dict(kv="head", hq=32, d=64), dict(kv="head", d=256),
+                                dict(kv="block", spread=3), dict(kv="block", hq=32, bs=32)])
+def test_values_that_are_no_numbers_reach_the_rows_that_see_them(kw, masks):
+    # elements of V, in the element of the output alone: of nodes, the rows whose masks have them,
+    # of the context, all of the sequence's (trees of one tile and two, items of one part and more)
+    seqs = [(200, 20), (9000, 5), (0, 17), (40, 70), (120, 16), (1300, 33)]
+    c = Case(60, seqs, masks=masks, pad=2, **kw)
+    ref = c.want()
+    d, hkv = c.q.shape[2], c.k.shape[1]
+    group = c.q.shape[1] // hkv
+    odd = [float("inf"), -float("inf"), float("nan")] if kw["kv"] == "same" else [float("nan")]
+    want = ref.out.clone()
+    spots = [(n, p + m, k) for n, (p, l) in enumerate(seqs) for k, m in enumerate(range(0, l, 3)) if n != 4]
+    spots += [(4, 120, 0), (4, 121, 1), (4, 135, 2), (1, 4000, 0), (5, 1299, 0)]     # (5: a context's last)
+    for n, pos, k in spots:
+        P0 = seqs[n][0]
+        rows = sees(c, n, pos - P0)
+        if not bool(rows.any()):
+            continue                                          # (NaN already)
+        for head in range(hkv):
+            col, x = (7 * k + 13 * n + 5 * head) % d, odd[(k + n + head) % len(odd)]
+            at = int(c.tables[n, pos // c.k.shape[2]]), head, pos % c.k.shape[2]
+            c.v[at][col] = x
+            want[rows, head * group:(head + 1) * group, col] += x
+    out, lse = c.run()
+    ok()
+    assert (out[-2:] == 9).all()
+    out, want, tol = out[:-2].double(), want[:-2], R.tolerance(ref, c.q.dtype, c.p_dtype)[:-2]
+    # (an infinity comes out as itself or, where a copy of the row or a part of the item has no weight
+    # for its key, as NaN)
+    assert torch.equal(out.isfinite(), want.isfinite()) and out[want.isnan()].isnan().all()
+    assert (out[out.isinf()] == want[out.isinf()]).all()
+    near = (out - want).abs() <= tol
+    assert near[want.isfinite()].all()
+    assert ((lse.double() - ref.lse).abs()[:-2] <= R.lse_tolerance(ref)[:-2])[ref.lse[:-2].isfinite()].all()
+
+
+@pytest.mark.parametrize("kw", [dict(kv="same"), dict(kv="same", dtype="f16", d=64, hq=32), dict(kv="same", d=256),
+                                dict(kv="head"), dict(kv="head", d=256), dict(kv="block", spread=3, hq=32)])
+def test_keys_that_are_no_numbers_reach_the_rows_that_see_them(kw):
+    # NaN, or a score of +inf: NaN in the row's out and lse; a score of -inf: no weight; rows that
+    # do not see the key, as if it were not there
+    seqs = [(200, 20), (9000, 5), (3, 17), (40, 70), (130, 33), (77, 50)]
+    c = Case(61, seqs, masks="tree", **kw)
+    bad = torch.zeros(c.q.shape[:2], dtype=torch.bool, device="cuda")
+    without = c.masks.clone()
+    for n, (m, x) in enumerate(((7, "nan"), (2, "inf"), (15, "-inf"), (64, "nan"), (13, "inf"), (31, "-inf"))):
+        x = float(x) if kw["kv"] == "same" else float("nan")
+        pos = seqs[n][0] + m
+        c.k[int(c.tables[n, pos // c.k.shape[2]]), :, pos % c.k.shape[2], 5] = x
+        rows = sees(c, n, m)
+        bad |= rows[:, None] & ~(c.q[:, :, 5].float() * x == -float("inf"))
+        without[rows.cpu(), m] = False
+    out, lse = c.run()
+    ok()
+    assert bad.any() and out[bad].isnan().all() and lse[bad].isnan().all()
+    ref = T.attention(c.q, c.k, c.v, c.tables, c.seq_lens, c.cu, c.scale, without, c.ks, c.vs)
+    assert ((out.double() - ref.out).abs() <= R.tolerance(ref, c.q.dtype, c.p_dtype))[~bad].all()
+    assert ((lse.double() - ref.lse).abs() <= R.lse_tolerance(ref))[~bad].all()
