@@ -735,6 +735,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
           }
         }
         wait(&s_bar[b], (u / NSB) & 1);
+        __syncwarp();
         tc::fence_after();
         if (u == u0) {
           sl2 = p.qk_scale_log2;                        // undoes the row's q scaling
@@ -777,6 +778,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
             mxw = fmaxf(mxw, top + ev);
             // a NaN K scale that the row sees makes its sum NaN, a V scale its P (below)
             if ((bytes & 0xFFu) == 255u && seen != 0u) l = __int_as_float(0x7FFFFFFF);
+            __syncwarp();
           }
         }
         // the row's maximum over the groups, as both its threads see it
@@ -802,6 +804,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
         if (u > u0 && __any_sync(0xFFFFFFFFu, scales_o)) {
           // O must hold every earlier tile before it is scaled, by each group its columns
           wait(&o_bar[(u - 1) % NSB], ((u - 1) / NSB) & 1);
+          __syncwarp();
           tc::fence_after();
 #pragma unroll 1
           for (int k = 0; k < COLS; k += 16) {
@@ -844,6 +847,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < kBS / 2; ++c) pv[c] = 0x7FFF7FFFu;
           }
+          if constexpr (BSC) __syncwarp();
           tc::st8(half + 8 * i, pv);
         }
         l = l * l_alpha + sum;
@@ -867,6 +871,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
       if constexpr (!KV8 || BSC) then.next();
       if constexpr (BSC) first_bytes(then);
       wait(&o_bar[last % NSB], (last / NSB) & 1);
+      __syncwarp();
       tc::fence_after();
       const bool whole = w.cnt == w.s.kt;               // else: a part, for the merge
       float lse = !(l == 0.f) ? m_ref + tree_lg2(l) : -INFINITY;
@@ -899,6 +904,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
 #pragma unroll 1
       for (int c = grp * COLS; c < (grp + 1) * COLS; c += 16) {
         uint32_t v[16];
+        __syncwarp();                                   // (rows that are none went on)
         tc::ld16(tO + lanes + c, v);
         tc::wait_ld();
         float o[16];
