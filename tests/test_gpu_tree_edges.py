@@ -6,7 +6,7 @@ import torch
 import paged_kv_decode_11_gb300 as P
 from tests import ext_ref as R
 from tests import tree_ref as T
-from tests.test_gpu_tree import Case, ok
+from tests.test_gpu_tree import QLEN, Case, ok
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +121,53 @@ def test_keys_that_are_no_numbers_reach_the_rows_that_see_them(kw):
     ref = T.attention(c.q, c.k, c.v, c.tables, c.seq_lens, c.cu, c.scale, without, c.ks, c.vs)
     assert ((out.double() - ref.out).abs() <= R.tolerance(ref, c.q.dtype, c.p_dtype))[~bad].all()
     assert ((lse.double() - ref.lse).abs() <= R.lse_tolerance(ref))[~bad].all()
+
+
+@pytest.mark.parametrize("kv", ["same", "head", "block"])
+def test_what_was_no_number_is_forgotten_by_the_next_call(kv):
+    # eager, and replayed from a graph, with a workspace that another call has used in between
+    c, other = Case(62, [(700, 20), (9000, 9), (60, 40)], kv=kv), Case(63, [(3000, 12)], kv=kv)
+    ws = torch.empty(P.paged_attn_tree_workspace_size(8, 2, 128), dtype=torch.uint8, device="cuda")
+    clean = c.run(lse=False, workspace=ws)[0].clone()
+    out = torch.empty_like(clean)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(lse=False, out=out, workspace=ws)
+    spots = [(int(c.tables[n, pos // 16]), slice(None), pos % 16, 3) for n, pos in ((0, 703), (1, 9008), (2, 65))]
+    was = [c.v[s].clone() for s in spots]
+    for call in (graph.replay, lambda: c.run(lse=False, out=out, workspace=ws)):
+        for s in spots:
+            c.v[s] = float("nan")
+        call()
+        seen = torch.stack([sees(c, n, m) for n, m in ((0, 3), (1, 8), (2, 5))]).any(0)
+        assert torch.equal(out[:, :, 3].isnan(), seen[:, None].expand(-1, 8))
+        assert torch.equal(torch.where(out.isnan(), clean, out), clean)
+        for s, x in zip(spots, was):
+            c.v[s] = x
+        other.run(workspace=ws)
+        call()
+        assert torch.equal(out, clean)
+    ok()
+
+
+def test_sequences_beside_refused_ones():
+    def values(c, rows, skip):
+        out, lse = c.run()
+        torch.cuda.synchronize()
+        assert P.pkv_get_device_error() == QLEN
+        ref = c.want(skip)
+        for r in rows:
+            c.check((out, lse), ref, r)
+        return out, lse
+
+    seqs = [(40, 10), (30, 6), (700, 7)]
+    c = Case(16, seqs)
+    c.cu[3] = 60                                              # past the rows of q
+    out, lse = values(c, [slice(0, 16)], (2,))
+    assert (out[16:] == 9).all() and (lse[16:] == 9).all()
+    # offsets that fall: the first sequence's tree of 17 nodes, the second's of -1, and one row
+    # that the first and the third both write
+    c = Case(16, seqs)
+    c.masks = torch.nn.functional.pad(c.masks, (0, 22))
+    c.cu[1] = 17
+    values(c, [slice(0, 16), slice(17, 23)], (1,))
