@@ -553,7 +553,8 @@ size_t paged_attn_tree_workspace_size(int num_q_heads, int num_kv_heads, int hea
  *   v_scales uint8 [num_blocks, Hkv]). Positions play no part: rotate queries and keys
  *   by the nodes' depths first.
  *   A row that sees nothing gives out = 0 and lse = -inf. L_n = 0 is fine; rows outside
- *   every sequence are left alone. out is not q, nor overlaps it. out_lse: optional fp32 [total_q_tokens, Hq].
+ *   every sequence are left alone. out is not q, nor overlaps it. out_lse: optional fp32
+ *   [total_q_tokens, Hq]. No cap, window, bias or prefix: those are the _ext calls'.
  *   What a row does not see does not reach it, whatever it is. A NaN or an infinity in an
  *   element of V comes out in that element of the rows that see its key (an infinity from
  *   before the tree perhaps as NaN). A score of NaN or +infinity (from q, K or a K scale of
@@ -581,10 +582,11 @@ pkv_status paged_attn_tree(void* out, const void* q, pkv_dtype q_dtype, const vo
  * to the front of the tree's places, in the K and V caches of every layer, so that the
  * sequence goes on as if it had never had another branch.
  *   k_caches, v_caches: HOST arrays of num_layers device pointers, each cache
- *           [num_blocks, Hkv, BS, D] and listed once. k_scales, v_scales: with PKV_FP8_E4M3_BLOCK, HOST
- *           arrays of num_layers pointers to uint8 [num_blocks, Hkv]; otherwise ignored
- *           (a scale per head moves with no token). The block tables are the layers' own
- *           common ones. Pointers are read before the call returns.
+ *           [num_blocks, Hkv, BS, D] and listed once (num_layers = 0: new_seq_lens alone).
+ *           k_scales, v_scales: with PKV_FP8_E4M3_BLOCK, HOST arrays of num_layers pointers
+ *           to uint8 [num_blocks, Hkv]; otherwise ignored (a scale per head moves with no
+ *           token). The block tables are the layers' own common ones. Pointers are read
+ *           before the call returns.
  *   Trees as for paged_attn_tree: sequence n has L_n = cu_q_lens[n+1] - cu_q_lens[n] nodes
  *           at positions P_n .. seq_lens[n] - 1.
  *   paths: int32 [num_seqs, max_path], path_lens: int32 [num_seqs]: of sequence n the

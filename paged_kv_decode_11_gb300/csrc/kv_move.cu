@@ -5,7 +5,7 @@
 // so that what bounds them is the memory's rate, and for a step's few tokens the latency of
 // a launch and of the look-ups in front of the first load: lengths, path and table. 96 blocks of
 // 32 KB in 64 caches take 61 us (6.6 TB/s, read and written), one block 4.0, a path of 13 in 64
-// caches 4.3; 64 paths of up to 60 in 32 block-scaled caches 17.5.
+// caches 4.5; 64 paths of up to 60 in 32 block-scaled caches 18.0.
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <climits>
@@ -188,9 +188,9 @@ __device__ __forceinline__ uint4 rescale16(uint4 w, int d) {
 }
 
 // Block scales. A warp has a (cache, KV head) pair of one sequence; the path's places are looked up
-// once for a CTA's eight. (64 paths in 32 caches of 8 heads: 17.5 us; with two pairs a warp 19.7,
-// with three 23.4; with eight chunks to a lane, 80 registers and so three CTAs an SM instead of
-// five, 21.5.) A warp goes from destination block to destination block (none of the path's later
+// once for a CTA's eight. (64 paths in 32 caches of 8 heads: 18.0 us. When one pair a warp took
+// 17.5, two took 19.7, three 23.4, and eight chunks to a lane, 80 registers and so three CTAs an
+// SM instead of five, 21.5.) A warp goes from destination block to destination block (none of the path's later
 // sources lies in an earlier one): it reads the path's rows there, reduces their exponents, and
 // writes them with the block's new one.
 // A block's rows of more than 128 16-byte chunks are read twice, for the exponent and to be

@@ -8,9 +8,11 @@
 // does not matter), a cluster barrier, then every CTA looks over its part of the counts, 16
 // a thread in flight, and the CTAs' totals go through each other's shared memory. A place's
 // rank finds its row by bisection of the rows' running sums, held in shared memory.
-// What bounds it is latency: three or four dependent trips to L2 and two or three barriers. Blocks
-// of 16: one row by 64 tokens 4.0 us, 256 rows by up to 600 tokens with 131,072 counts 12.6; a
-// prompt of 900 into four rows 8.2, 256 rows of up to 8,192 tokens with 98,304 counts 19.4.
+// What bounds it is latency: of a resize two or three dependent trips to L2 (lengths, counts, for
+// rows that shrink entries) and two cluster barriers; of a fork six (lengths and parents, last
+// entries, tables, tables again, counts, the copies' sources) and three. Blocks of 16: one row by
+// 64 tokens 4.1 us, 256 rows by up to 600 tokens with 131,072 counts 12.7; a prompt of 900 into
+// four rows 8.5, 256 rows of up to 8,192 tokens with 98,304 counts 19.9.
 #include <cuda_runtime.h>
 #include <atomic>
 #include "launch_pages.h"

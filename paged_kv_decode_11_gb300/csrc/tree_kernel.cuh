@@ -38,12 +38,13 @@
 //
 // What bounds it (GB300, 32 query heads on 8 KV heads of 128): 16-bit caches, the bandwidth:
 // another tile costs an SM 1.5 us, 6.6 TB/s over all; eight contexts of 16,384 with trees of 16
-// take 95 us (5.7 TB/s), 32 of 4,096 103 us (5.2), 128 of 1,024 119 us (4.6). 8-bit caches, the
+// take 97 us (5.5 TB/s), 32 of 4,096 104 us (5.2), 128 of 1,024 121 us (4.5). 8-bit caches, the
 // conversion: 1.25 to 1.4 us a tile (1.75 with block scales and 128 rows, whose softmax has most
 // to do), where the bandwidth alone would take 0.75; of that 1,800 cycles are traffic of shared
-// memory (staged, read, written as f16, read by the MMAs): the same three shapes take 91, 98 and
-// 130 us with a scale per head. Beside the tiles a call costs some 12 us of latencies that follow
-// one another (17 with an 8-bit cache), and a segment 3 us and more.
+// memory (staged, read, written as f16, read by the MMAs): the same three shapes take 85, 98 and
+// 132 us with a scale per head, 91, 104 and 139 with block scales. Beside the tiles a call costs
+// some 12 us of latencies that follow one another (17 with an 8-bit cache), and a segment 3 us
+// and more.
 #pragma once
 #include "block_scale.cuh"
 #include "tc.cuh"
@@ -74,9 +75,9 @@ struct TreeCfg {
   static constexpr int SMEM_BYTES = Q_BYTES + 2 * NST * KV_BYTES + 2 * NSS * STG_BYTES;
   static constexpr uint32_t TMEM_COLS = 512;
   // What a segment costs beside its tiles, in tiles, for the ranges' lengths. (0, 2, 3, 4, 6 and 8
-  // tiles: 108, 66, 61, 59, 59 and 64 us on 64 contexts of 100 to 1,500 tokens; 200, 168, 163, 163,
-  // 166 and 167 us on 64 of 1,024 to 8,192; with block scales 123, 81, 74, 71, 74 and 79 us and 210,
-  // 179, 169, 163, 165 and 170 us.)
+  // tiles: 114, 75, 66, 66, 67 and 70 us on 64 contexts of 100 to 1,500 tokens; 231, 212, 209, 208,
+  // 209 and 209 us on 64 of 1,024 to 8,192; with block scales 135, 88, 77, 74, 76 and 80 us and 244,
+  // 218, 214, 208, 204 and 205 us. D = 128; at 256, where a tile is 64 keys, it was not measured.)
   static constexpr int COST = 4;
   static_assert(KEYS == NG * HALF, "a half of a tile to each group");
   static_assert(NSB * KEYS + D <= (int)TMEM_COLS, "tensor memory");
@@ -867,7 +868,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
       // item over its copies (those of a part stay apart) ------------------------------------
       const int last = u0 + w.cnt - 1;
       Work then = w;
-      // (not yet for a scale per head: there it gains nothing, and its code costs 2%)
+      // (not yet for a scale per head: 368 us on four contexts of 80,000, where later takes 362)
       if constexpr (!KV8 || BSC) then.next();
       if constexpr (BSC) first_bytes(then);
       wait(&o_bar[last % NSB], (last / NSB) & 1);
@@ -934,8 +935,8 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
       if (whole && reps > 1) {
         // the copies' sum: a thread takes a row's columns of group and copy, 2 or 4 copies each,
         // the loads BATCH at a time (one after the other they cost an item 3 us). 16 at a time take
-        // 122 us on 128 contexts of 1,024, where 4 take 125; with an E4M3 cache 132 and 133, but
-        // their code costs four contexts of 80,000 372 us, where 4 at a time take 362.
+        // 121 us on 128 contexts of 1,024, where 4 take 125; with a scale per head 130 and 132, but
+        // with block scales 92 us on eight contexts of 16,384, where 4 at a time take 91.
         named_barrier(1, Cfg::SOFT);
         constexpr int EACH = D / 4 / NG;                // float4 of a row to load, all copies'
         constexpr int BATCH = KV8 ? 4 : EACH < 16 ? EACH : 16;

@@ -6,10 +6,11 @@
 // columns of this kernel's blocks, one for each place, and their warps take its (32 rows, 4
 // columns) units in turn, so that a cut costs the same wherever it falls; a lane is a row, and
 // every load of a warp is 512 consecutive bytes. What bounds it is the latency of its loads:
-// BATCH parts' are under way together. Eight, with three CTAs an SM (32 sequences
-// on 4 KV heads of 1,280 tokens, with the attention, 48 us, where 16 take 52; 128 on 8 heads of 1,024
-// 119 and 122); 16 where there are so few sequences and heads that an item is cut into four
-// parts and more (one of 900 tokens on 8 heads 13.1 us, where 8 take 13.7; of 8,000 18.3 and 19.2).
+// BATCH parts' are under way together. Eight, with three CTAs an SM (32 sequences on 4 KV heads
+// of 1,280 tokens, with the attention, 51 us, where 16 take 56; 128 on 8 heads of 1,024 121 and
+// 124); 16 where there are so few sequences and heads that an item is cut into four parts and more
+// (one of 900 tokens on 8 heads 12.4 us, where 8 take 12.8; of 8,000 22.2 and 23.1. The rule
+// counts no row tiles: the host knows no tree's size).
 //   Elements of V in a tree that are no numbers, which the attention took for 0, are added here to
 // the outputs of the rows that see their keys, for every item: a weight of 0 in the attention's
 // product would not keep them from the other rows. (There it cost the E4M3 kernels 2 to 4%, in

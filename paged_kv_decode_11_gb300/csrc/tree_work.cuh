@@ -75,8 +75,9 @@ struct TreeWork {
     return w;
   }
   // The next segment. Six places take it, in 3 KB of code each: with an E4M3 cache, whose
-  // producers have more code than a copy, out of line (379 us on four contexts of 80,000 of 8
-  // bits, so 366; a small tree over 16 bits 13.2 us, so 13.7).
+  // producers have more code than a copy, out of line (365 us on four contexts of 80,000 of 8
+  // bits, so 361, and 93 on eight of 16,384 with block scales, so 91; but 128 of 1,024 with a scale
+  // per head 128, so 132. A small tree over 16 bits 12.4 us, so 12.7, and 128 of 1,024 121, so 124).
   __device__ __forceinline__ void next() {
     if constexpr (OUT_OF_LINE) *this = stepped(*this);
     else step();

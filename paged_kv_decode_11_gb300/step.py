@@ -275,9 +275,10 @@ class TreeStep:
 
     q, new_k, new_v: [tokens, heads, D] of all sequences' nodes in order, cu_q_lens [n + 1] their
     offsets, seq_lens including them; tree_masks as paged_attn_tree takes them (None: chains).
-    Queries and keys come rotated, by the nodes' depths. The cache is 16-bit or E4M3 with a scale
-    per KV head (new_slots int64: the nodes' slots) or E4M3 with block scales (k_scales, v_scales
-    [num_blocks, Hkv]: the nodes are appended). Every call works on the buffers given here, so
+    Queries and keys come rotated, by the nodes' depths: no call here does it, as a node's depth
+    is not its place. The cache is 16-bit or E4M3 with a scale per KV head (new_slots int64: the
+    nodes' slots) or E4M3 with block scales (k_scales, v_scales [num_blocks, Hkv]: the nodes are
+    appended). No cap, window or bias of scores. Every call works on the buffers given here, so
     that a step can be captured into a CUDA graph and replayed with new contents."""
 
     def __init__(self, k_cache, v_cache, q, new_k, new_v, block_tables, seq_lens, cu_q_lens, scale,
@@ -313,8 +314,8 @@ class TreeStep:
         self.attend(stream)
 
     def keep(self, paths, path_lens, new_seq_lens=None, stream=None):
-        """The nodes paths[n, :path_lens[n]] stay, as the tokens behind the context; new_seq_lens
-        <- the lengths then."""
+        """The nodes paths[n, :path_lens[n]] stay, as the tokens behind the context, in this layer's
+        cache; new_seq_lens <- the lengths then. (One kv_keep_path moves them in every layer's.)"""
         scaled = (self.k_scales, self.v_scales) if self.block_scaled else (None, None)
         B.kv_keep_path(self.k_cache, self.v_cache, self.block_tables, self.seq_lens,
                        self.cu_q_lens, paths, path_lens, *scaled, new_seq_lens=new_seq_lens,
