@@ -71,11 +71,15 @@ struct TreeParams {
   float qk_scale_log2;
 };
 
-// Workspace: ctas * (three partial results, a TreeSplit, a TreeOdd), and a TreeSplit that is empty.
+// Workspace: ctas * (three partial results, a TreeSplit, a TreeOdd), and a TreeSplit that is empty;
+// 0 without a device.
 constexpr size_t tree_part_floats(int head_dim) { return (size_t)kTreeRows * head_dim; }
 constexpr size_t tree_workspace_bytes(int ctas, int head_dim) {
-  return (size_t)ctas * (kTreeParts * (tree_part_floats(head_dim) + kTreeRows) * sizeof(float) +
-                         sizeof(TreeSplit) + sizeof(TreeOdd)) + sizeof(TreeSplit);
+  return ctas == 0 ? 0
+                   : (size_t)ctas * (kTreeParts * (tree_part_floats(head_dim) + kTreeRows) *
+                                         sizeof(float) +
+                                     sizeof(TreeSplit) + sizeof(TreeOdd)) +
+                         sizeof(TreeSplit);
 }
 
 // Validate nothing (the entry point does); PKV_ERR_CUDA on a launch failure. A call is two
