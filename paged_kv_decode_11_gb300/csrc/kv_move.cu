@@ -190,9 +190,9 @@ __device__ __forceinline__ uint4 rescale16(uint4 w, int d) {
 // Block scales. A warp has a (cache, KV head) pair of one sequence; the path's places are looked up
 // once for a CTA's eight. (64 paths in 32 caches of 8 heads: 18.0 us. When one pair a warp took
 // 17.5, two took 19.7, three 23.4, and eight chunks to a lane, 80 registers and so three CTAs an
-// SM instead of five, 21.5.) A warp goes from destination block to destination block (none of the path's later
-// sources lies in an earlier one): it reads the path's rows there, reduces their exponents, and
-// writes them with the block's new one.
+// SM instead of five, 21.5.) A warp goes from destination block to destination block (none of the
+// path's later sources lies in an earlier one): it reads the path's rows there, reduces their
+// exponents, and writes them with the block's new one.
 // A block's rows of more than 128 16-byte chunks are read twice, for the exponent and to be
 // written, the rows in order, so that none is overwritten before it is read.
 constexpr int kKeepWarps = 8, kKeepChunks = 4;          // chunks of a lane at a time
