@@ -716,6 +716,11 @@ __global__ void __launch_bounds__(TreeCfg<D, KV == KV_E4M3>::THREADS, 1)
             // V of the tree and of what lies behind it: zeros for what is no number, as a weight
             // of 0 does not keep it from a row (the rows that see it get it at the end)
             const int st = u % NST, from = max(P - t * KEYS, 0);
+            // The stage's tile before, u - NST, first: a barrier tells only the last phase from the
+            // one under way, and tile u - NST may not have landed, let alone been multiplied, when a
+            // warp comes here (S(u - 1) waited for P.V of u - 4 alone, and NST may be 2)
+            static_assert(NSB == 3 && NST >= 2, "P.V of u - 2 NST is done");
+            if (u >= NST) wait(&empty_v[st], ((u / NST) - 1) & 1);
             wait(&full_v[st], (u / NST) & 1);
 #pragma unroll 1
             for (int i = tid; i < (KEYS - from) * Cfg::NBOX * 8; i += Cfg::SOFT) {

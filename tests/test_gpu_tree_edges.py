@@ -1,5 +1,6 @@
 """paged_attn_tree where its softmax and its masks are at their limits, against attention in 64 bits
 (tests/tree_ref.py, tolerances of tests/ext_ref.py)."""
+import numpy as np
 import pytest
 import torch
 
@@ -171,3 +172,20 @@ def test_sequences_beside_refused_ones():
     c.masks = torch.nn.functional.pad(c.masks, (0, 22))
     c.cu[1] = 17
     values(c, [slice(0, 16), slice(17, 23)], (1,))
+
+
+@pytest.mark.parametrize("masks", ["tree", "random"])
+@pytest.mark.parametrize("kw", [dict(d=256), dict(d=256, dtype="f16", hq=25, hkv=5, bs=64), dict(d=256, hq=64, hkv=8),
+                                dict(d=128, hkv=5, hq=15), dict(d=128, dtype="f16", hq=32, bs=32), dict(d=64, hq=32),
+                                dict(kv="head", d=256), dict(kv="block", hq=32)])
+def test_segments_of_few_tiles(kw, masks):
+    # tails of trees a tile or two behind one another, in ring stages that the tiles before have
+    # just left or not yet reached: what lies behind a context, and nodes that nobody sees, are NaN
+    rng = np.random.default_rng(70)
+    for seed in range(6):
+        seqs = [(int(rng.choice([0, 1, 15, 63, 64, 127, 128, 129, 500])), int(rng.integers(1, 66)))
+                for _ in range(int(rng.integers(5, 60)))]
+        c = Case(70 + seed, seqs, masks=masks, pad=seed % 2, qsize=float(2.0 ** rng.integers(-3, 3)), **kw)
+        got = c.run()
+        ok()
+        c.check(got)
